@@ -403,6 +403,136 @@ MAO_API mao_status adamw_step(void* w, int32_t w_dtype, const void* g, int32_t g
                       float eps, float weight_decay, float* update_out, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Layer operators: what makes the gradients that the steps consume           */
+/* ------------------------------------------------------------------------ */
+/*
+ * Layer norm, the linear layer with its epilogue, and 8-bit activation
+ * checkpoints, each with its backward pass: the calls of a pre-norm MLP (or
+ * projection) layer whose weight gradients dW go to muon_step, soap_step or
+ * foam_step and whose bias and norm gradients go to adamw_step.
+ *
+ * The conventions above hold (row-major views, ld a multiple of 8, caller-owned
+ * buffers, host-side validation, no synchronisation, bitwise repeatable).
+ * Vectors (gamma, beta, bias) are contiguous and 16-byte aligned, fp32 or bf16;
+ * statistics and vector gradients are fp32. Storage between cols and the next
+ * multiple of 8 of a row may be read and is never written. Arithmetic and sums
+ * are fp32; each result is rounded once, as it is stored. Sizes are at least 1
+ * (MAO_E_SHAPE) and at most 2^20.
+ */
+
+/* 8-bit activation checkpoint of a rows x cols matrix: one code per element
+ * (row-major, leading dimension ld, a multiple of 32, 16-byte aligned) and one
+ * scale byte s per row and 32 columns (leading dimension ld_scale >= ceil(cols /
+ * 32)). An element is code * 2^(s - 127): s is the smallest exponent (at
+ * least 1, 3 for e4m3) that keeps every code of the 32 in range, so each stored
+ * value is exact in bf16. s = 0
+ * marks 32 zeros; s = 255 marks 32 elements that held a NaN or an infinity,
+ * which all read as NaN. */
+typedef enum {
+  MAO_Q8_INT8 = 0, /* |code| <= 127, round to nearest even */
+  MAO_Q8_E4M3 = 1  /* OCP fp8 e4m3 (largest 448), round to nearest even */
+} mao_q8_format;
+
+typedef struct {
+  void* codes;
+  uint8_t* scales;
+  int64_t rows, cols, ld, ld_scale;
+  int32_t format; /* mao_q8_format */
+} mao_q8;
+
+/* Activations: relu, z Phi(z) (gelu), its tanh form 0.5 z (1 + tanh(sqrt(2/pi) (z +
+ * 0.044715 z^3))), z / (1 + exp(-z)) (silu). */
+typedef enum {
+  MAO_ACT_NONE = 0,
+  MAO_ACT_RELU = 1,
+  MAO_ACT_GELU = 2,
+  MAO_ACT_GELU_TANH = 3,
+  MAO_ACT_SILU = 4
+} mao_act;
+
+/* mao_q8_quantize -- X8 <- X (bf16 or fp32), X8's rows and cols those of X. */
+MAO_API mao_status mao_q8_quantize(mao_mat X, const mao_q8* X8, void* stream);
+
+/* mao_q8_dequantize -- Y <- act(X8), Y bf16 or fp32. */
+MAO_API mao_status mao_q8_dequantize(const mao_q8* X8, int32_t act, mao_mat Y, void* stream);
+
+/*
+ * mao_layer_norm -- over each row of X (cols <= 32768, MAO_E_UNSUPPORTED above):
+ *   mean = sum x / cols;  rstd = (sum (x - mean)^2 / cols + eps)^(-1/2)
+ *   y = (x - mean) rstd gamma + beta
+ * gamma, beta: NULL (1, 0) or cols values of param_dtype. mean, rstd: NULL or
+ * rows floats, kept for the backward pass. X, Y: bf16 or fp32 each; eps > 0.
+ */
+MAO_API mao_status mao_layer_norm(mao_mat X, const void* gamma, const void* beta,
+                                  int32_t param_dtype, float eps, mao_mat Y, float* mean,
+                                  float* rstd, void* stream);
+
+MAO_API size_t mao_layer_norm_backward_workspace_size(int64_t rows, int64_t cols);
+
+/*
+ * mao_layer_norm_backward -- with xh = (x - mean) rstd and g = dy gamma:
+ *   dX = rstd (g - mean(g) - xh mean(g xh)) [+ add]
+ *   dgamma = sum over rows of dy xh;  dbeta = sum over rows of dy
+ * The input is X, or its checkpoint X8 (exactly one of the two, the other
+ * NULL). add: NULL, or a gradient that joins dX (the skip connection's); it may
+ * be dX itself. dgamma, dbeta: each NULL or cols floats; the workspace is only
+ * needed for them.
+ */
+MAO_API mao_status mao_layer_norm_backward(mao_mat dY, const mao_mat* X, const mao_q8* X8,
+                                           const void* gamma, int32_t param_dtype,
+                                           const float* mean, const float* rstd,
+                                           const mao_mat* add, mao_mat dX, float* dgamma,
+                                           float* dbeta, void* workspace, size_t workspace_bytes,
+                                           void* stream);
+
+/* Workspace bytes of the three linear calls for X rows x k, W n x k of dtype
+ * (0 when none is needed or an argument is invalid). */
+MAO_API size_t mao_linear_workspace_size(int64_t rows, int64_t k, int64_t n, int32_t dtype);
+MAO_API size_t mao_linear_backward_input_workspace_size(int64_t rows, int64_t k, int64_t n,
+                                                        int32_t dtype);
+/* rebuilt != 0: the input comes from a checkpoint or through x_act. */
+MAO_API size_t mao_linear_backward_weight_workspace_size(int64_t rows, int64_t k, int64_t n,
+                                                         int32_t dtype, int32_t rebuilt);
+
+/*
+ * mao_linear -- Z = X W^T + bias;  Y = act(Z) + residual.
+ * X: rows x k, W: n x k, one dtype (bf16: bf16 matrix cores, exact products;
+ * fp32: fp32 matrix cores). bias: NULL or n values of bias_dtype. residual:
+ * NULL or rows x n, may be Y itself. preact: NULL or rows x n receiving Z. Y,
+ * residual and preact: bf16 or fp32 each.
+ */
+MAO_API mao_status mao_linear(mao_mat X, mao_mat W, const void* bias, int32_t bias_dtype,
+                              int32_t act, const mao_mat* residual, mao_mat Y,
+                              const mao_mat* preact, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/*
+ * mao_linear_backward_input -- dX = (dY W) . act'(z) [+ add].
+ * dY: rows x n and W: n x k, one dtype. z: the pre-activation that act was
+ * applied to before this layer (rows x k), as a tensor Z or its checkpoint Z8
+ * (exactly one unless act is MAO_ACT_NONE, then neither): dX is then the
+ * gradient of that pre-activation. add: NULL or rows x k, may be dX itself.
+ */
+MAO_API mao_status mao_linear_backward_input(mao_mat dY, mao_mat W, int32_t act, const mao_mat* Z,
+                                             const mao_q8* Z8, const mao_mat* add, mao_mat dX,
+                                             void* workspace, size_t workspace_bytes,
+                                             void* stream);
+
+/*
+ * mao_linear_backward_weight -- dW = dY^T a [+ dW];  dbias = sum over rows of dY
+ * [+ dbias], with a = x_act(X) (rows x k). The layer's input is X (dY's dtype)
+ * or its checkpoint X8 (exactly one); x_act recomputes an activation that was
+ * not kept. Against a bf16 dY, a is rounded to bf16, as the forward product
+ * read it (without x_act a checkpoint's values are exact in bf16). dW: n x k,
+ * bf16 or fp32; dbias: NULL or n floats. accumulate != 0 adds to both (the
+ * micro-batches of one step).
+ */
+MAO_API mao_status mao_linear_backward_weight(mao_mat dY, const mao_mat* X, const mao_q8* X8,
+                                              int32_t x_act, mao_mat dW, float* dbias,
+                                              int32_t accumulate, void* workspace,
+                                              size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Building blocks exposed for kernel-level checks                           */
 /* ------------------------------------------------------------------------ */
 

@@ -1,4 +1,6 @@
-"""Matrix-aware optimizer steps (Muon, Muon+, SOAP, FOAM, AdamW) on AMD MI355X.
+"""Matrix-aware optimizer steps (Muon, Muon+, SOAP, FOAM, AdamW) on AMD MI355X,
+and the layer operators that make their gradients (layer norm, linear layer,
+8-bit activation checkpoints).
 
 Thin ctypes binding over ``libmao.so`` (declared in ``include/mao.h``). The
 binding only marshals arguments: every step runs in the library's HIP
@@ -64,7 +66,15 @@ class FoamHparams(ctypes.Structure):
                 ("refresh_prod", c_int32)]
 
 
+class Q8C(ctypes.Structure):
+    _fields_ = [("codes", c_void_p), ("scales", c_void_p), ("rows", c_int64), ("cols", c_int64),
+                ("ld", c_int64), ("ld_scale", c_int64), ("format", c_int32)]
+
+
 REFRESH_MODES = {"qr": 0, "eigh": 1}
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+Q8_FORMATS = {"int8": 0, "e4m3": 1}
+Q8_BLOCK = 32
 ROT_MODES = {"f32": 0, "bf16x3": 1}
 EIGH_MAX_SWEEPS = 12
 
@@ -105,6 +115,24 @@ EXPORTS = {
     "adamw_step": (c_int32, [c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_void_p, c_int64,
                              c_int64, c_float, c_float, c_float, c_float, c_float, c_void_p,
                              c_void_p]),
+    "mao_q8_quantize": (c_int32, [Mat, POINTER(Q8C), c_void_p]),
+    "mao_q8_dequantize": (c_int32, [POINTER(Q8C), c_int32, Mat, c_void_p]),
+    "mao_layer_norm": (c_int32, [Mat, c_void_p, c_void_p, c_int32, c_float, Mat, c_void_p,
+                                 c_void_p, c_void_p]),
+    "mao_layer_norm_backward_workspace_size": (c_size_t, [c_int64, c_int64]),
+    "mao_layer_norm_backward": (c_int32, [Mat, POINTER(Mat), POINTER(Q8C), c_void_p, c_int32,
+                                          c_void_p, c_void_p, POINTER(Mat), Mat, c_void_p,
+                                          c_void_p, c_void_p, c_size_t, c_void_p]),
+    "mao_linear_workspace_size": (c_size_t, [c_int64, c_int64, c_int64, c_int32]),
+    "mao_linear_backward_input_workspace_size": (c_size_t, [c_int64, c_int64, c_int64, c_int32]),
+    "mao_linear_backward_weight_workspace_size": (c_size_t, [c_int64, c_int64, c_int64, c_int32,
+                                                             c_int32]),
+    "mao_linear": (c_int32, [Mat, Mat, c_void_p, c_int32, c_int32, POINTER(Mat), Mat, POINTER(Mat),
+                             c_void_p, c_size_t, c_void_p]),
+    "mao_linear_backward_input": (c_int32, [Mat, Mat, c_int32, POINTER(Mat), POINTER(Q8C),
+                                            POINTER(Mat), Mat, c_void_p, c_size_t, c_void_p]),
+    "mao_linear_backward_weight": (c_int32, [Mat, POINTER(Mat), POINTER(Q8C), c_int32, Mat,
+                                             c_void_p, c_int32, c_void_p, c_size_t, c_void_p]),
     "mao_gemm_nt": (c_int32, [c_int64, c_int64, c_int64, c_float, c_void_p, c_int64, c_void_p,
                               c_int64, c_int32, c_float, c_void_p, c_int64, c_void_p, c_int64,
                               c_int32, c_void_p]),
@@ -417,6 +445,258 @@ def adamw_step(w, g, m, v, t: int, *, lr, beta1=0.9, beta2=0.95, eps=1e-8, weigh
     _check(lib.adamw_step(_ptr(w), dtype_code(w), _ptr(g), dtype_code(g), _ptr(m), _ptr(v),
                           w.numel(), t, lr, beta1, beta2, eps, weight_decay, _ptr(update_out),
                           _stream()), "adamw_step")
+
+
+# ---------------------------------------------------------------------------
+# layer operators
+# ---------------------------------------------------------------------------
+#
+# Matrices are 2-D tensors that meet the layout rule (``padded`` copies one that
+# does not, ``empty_matrix`` makes one). All work runs on the current stream of
+# the tensors' device. Results that are not passed in are allocated here.
+
+class Q8:
+    """8-bit checkpoint of a 2-D tensor: ``codes`` (int8 or float8_e4m3fn, row
+    stride a multiple of 32) and ``scales`` (uint8, one per row and 32 columns);
+    an element stands for code * 2 ** (scale - 127)."""
+
+    def __init__(self, codes, scales):
+        torch = _torch()
+        if codes.dtype == torch.int8:
+            fmt = 0
+        elif codes.dtype == torch.float8_e4m3fn:
+            fmt = 1
+        else:
+            raise TypeError(f"codes must be int8 or float8_e4m3fn, not {codes.dtype}")
+        if scales.dtype != torch.uint8:
+            raise TypeError("scales must be uint8")
+        if codes.dim() != 2 or codes.stride(1) != 1 or scales.dim() != 2 or scales.stride(1) != 1:
+            raise ValueError("codes and scales must be 2-D and row-major")
+        blocks = (codes.shape[1] + Q8_BLOCK - 1) // Q8_BLOCK
+        if scales.shape[0] != codes.shape[0] or scales.shape[1] < blocks:
+            raise ValueError("scales need one byte per row and 32 columns")
+        if scales.device != codes.device:
+            raise ValueError("codes and scales must share a device")
+        self.codes, self.scales = codes, scales
+        self.c = Q8C(codes.data_ptr(), scales.data_ptr(), codes.shape[0], codes.shape[1],
+                     codes.stride(0), scales.stride(0), fmt)
+
+    shape = property(lambda self: self.codes.shape)
+    device = property(lambda self: self.codes.device)
+    fmt = property(lambda self: "e4m3" if self.c.format else "int8")
+
+
+def q8_empty(rows, cols, fmt="int8", device=None) -> Q8:
+    """Uninitialised checkpoint storage for a rows x cols tensor."""
+    torch = _torch()
+    blocks = (cols + Q8_BLOCK - 1) // Q8_BLOCK
+    dt = (torch.int8, torch.float8_e4m3fn)[Q8_FORMATS[fmt]]
+    codes = torch.empty((rows, blocks * Q8_BLOCK), dtype=dt, device=device)
+    return Q8(codes[:, :cols], torch.empty((rows, blocks), dtype=torch.uint8, device=device))
+
+
+class _Device:
+    """The tensors' common device as current, its stream, and a workspace."""
+
+    def __init__(self, first, *rest):
+        torch = _torch()
+        dev = first.device
+        if dev.type != "cuda":
+            raise ValueError(f"tensors must be on the GPU, not on {dev}")
+        for t in rest:
+            if t is not None and t.device != dev:
+                raise ValueError(f"tensors on {dev} and {t.device}")
+        self.device = dev
+        self.guard = None
+        if dev.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        self.handle = _torch().cuda.current_stream(self.device).cuda_stream
+        self.stream = c_void_p(self.handle)
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+    def workspace(self, nbytes):
+        """(pointer, bytes) of a buffer that only this stream's calls share. Under
+        graph capture it is the graph's own, so that a later, larger call
+        cannot take it away from the graph."""
+        if nbytes == 0:
+            return None, 0
+        if _torch().cuda.is_current_stream_capturing():
+            self.buf = _torch().empty(nbytes, dtype=_torch().uint8, device=self.device)
+            return c_void_p(self.buf.data_ptr()), nbytes
+        key = (self.device.index, self.handle)
+        buf = _layer_ws.get(key)
+        if buf is None or buf.numel() < nbytes:
+            buf = _torch().empty(nbytes, dtype=_torch().uint8, device=self.device)
+            _layer_ws[key] = buf
+        return c_void_p(buf.data_ptr()), buf.numel()
+
+
+_layer_ws: dict = {}
+
+
+def _matp(t):
+    return None if t is None else ctypes.byref(mat(t))
+
+
+def _vec(t, n, name):
+    """(pointer, dtype code) of an optional contiguous vector of n values."""
+    if t is None:
+        return None, F32
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n} values")
+    return c_void_p(t.data_ptr()), dtype_code(t)
+
+
+def _floats(t, n, name):
+    p, code = _vec(t, n, name)
+    if code != F32:
+        raise TypeError(f"{name} must be float32")
+    return p
+
+
+def _act_code(act):
+    return ACTS[act] if isinstance(act, str) else int(act)
+
+
+def _split(x):
+    """(matrix pointer, checkpoint pointer) of a tensor, a Q8 or None."""
+    if isinstance(x, Q8):
+        return None, ctypes.byref(x.c)
+    return _matp(x), None
+
+
+def q8_quantize(X, fmt="int8", out=None) -> Q8:
+    """Keeps X (bf16 or fp32) in 8 bits."""
+    if out is None:
+        out = q8_empty(X.shape[0], X.shape[1], fmt, X.device)
+    with _Device(X, out) as d:
+        _check(load().mao_q8_quantize(mat(X), ctypes.byref(out.c), d.stream), "mao_q8_quantize")
+    return out
+
+
+def q8_dequantize(q: Q8, act="none", dtype=None, out=None):
+    """act(q) as a tensor (bf16 unless ``dtype`` or ``out`` says fp32)."""
+    if out is None:
+        out = empty_matrix(q.shape[0], q.shape[1], dtype or _torch().bfloat16, q.device)
+    with _Device(q, out) as d:
+        _check(load().mao_q8_dequantize(ctypes.byref(q.c), _act_code(act), mat(out), d.stream),
+               "mao_q8_dequantize")
+    return out
+
+
+def layer_norm(X, gamma=None, beta=None, *, eps=1e-5, out=None, stats=True):
+    """(Y, mean, rstd) of layer norm over the rows of X; the statistics are None
+    without ``stats``."""
+    torch = _torch()
+    rows, cols = X.shape
+    if out is None:
+        out = empty_matrix(rows, cols, X.dtype, X.device)
+    mean = rstd = None
+    if stats:
+        mean = torch.empty(rows, dtype=torch.float32, device=X.device)
+        rstd = torch.empty(rows, dtype=torch.float32, device=X.device)
+    g, gd = _vec(gamma, cols, "gamma")
+    b, bd = _vec(beta, cols, "beta")
+    if g is not None and b is not None and gd != bd:
+        raise TypeError("gamma and beta must share a dtype")
+    with _Device(X, gamma, beta, out) as d:
+        _check(load().mao_layer_norm(mat(X), g, b, gd if g is not None else bd, eps, mat(out),
+                                     _ptr(mean), _ptr(rstd), d.stream), "mao_layer_norm")
+    return out, mean, rstd
+
+
+def layer_norm_backward(dY, X, gamma, mean, rstd, *, add=None, out=None, dgamma=None, dbeta=None):
+    """(dX, dgamma, dbeta) of layer_norm. X: its input, or the input's Q8
+    checkpoint. ``add`` joins dX (the skip connection's gradient)."""
+    torch = _torch()
+    lib = load()
+    rows, cols = dY.shape
+    if out is None:
+        out = empty_matrix(rows, cols, dY.dtype, dY.device)
+    if dgamma is None:
+        dgamma = torch.empty(cols, dtype=torch.float32, device=dY.device)
+    if dbeta is None:
+        dbeta = torch.empty(cols, dtype=torch.float32, device=dY.device)
+    g, gd = _vec(gamma, cols, "gamma")
+    x, x8 = _split(X)
+    with _Device(dY, X, gamma, mean, rstd, add, out, dgamma, dbeta) as d:
+        ws, nws = d.workspace(lib.mao_layer_norm_backward_workspace_size(rows, cols))
+        _check(lib.mao_layer_norm_backward(
+            mat(dY), x, x8, g, gd, _floats(mean, rows, "mean"), _floats(rstd, rows, "rstd"),
+            _matp(add), mat(out), _floats(dgamma, cols, "dgamma"), _floats(dbeta, cols, "dbeta"),
+            ws, nws, d.stream), "mao_layer_norm_backward")
+    return out, dgamma, dbeta
+
+
+def linear(X, W, bias=None, *, act="none", residual=None, out=None, preact=None):
+    """act(X W^T + bias) + residual. ``preact``: a tensor that receives the value
+    before the activation; ``out`` may be ``residual``."""
+    lib = load()
+    rows, k = X.shape
+    n = W.shape[0]
+    if out is None:
+        out = empty_matrix(rows, n, X.dtype, X.device)
+    b, bd = _vec(bias, n, "bias")
+    mx = mat(X)
+    with _Device(X, W, bias, residual, out, preact) as d:
+        ws, nws = d.workspace(lib.mao_linear_workspace_size(rows, k, n, mx.dtype))
+        _check(lib.mao_linear(mx, mat(W), b, bd, _act_code(act), _matp(residual), mat(out),
+                              _matp(preact), ws, nws, d.stream), "mao_linear")
+    return out
+
+
+def linear_backward_input(dY, W, *, act="none", preact=None, add=None, out=None):
+    """(dY W) * act'(preact) + add: the gradient of the layer's input, taken back
+    through the activation that made it. ``preact``: a tensor or a Q8."""
+    lib = load()
+    rows, n = dY.shape
+    k = W.shape[1]
+    if out is None:
+        out = empty_matrix(rows, k, dY.dtype, dY.device)
+    code = _act_code(act)
+    z, z8 = _split(preact)
+    my = mat(dY)
+    with _Device(dY, W, preact, add, out) as d:
+        ws, nws = d.workspace(lib.mao_linear_backward_input_workspace_size(rows, k, n, my.dtype))
+        _check(lib.mao_linear_backward_input(my, mat(W), code, z, z8, _matp(add), mat(out), ws, nws,
+                                             d.stream), "mao_linear_backward_input")
+    return out
+
+
+def linear_backward_weight(dY, X, *, x_act="none", dtype=None, out=None, dbias=None,
+                           accumulate=False):
+    """(dW, dbias) = (dY^T x_act(X), column sums of dY). X: the layer's input or
+    its Q8 checkpoint. With ``accumulate`` both are added to ``out`` and
+    ``dbias``, which then have to be given."""
+    torch = _torch()
+    lib = load()
+    rows, n = dY.shape
+    k = X.shape[1]
+    if accumulate and (out is None or dbias is None):
+        raise ValueError("accumulate needs out and dbias")
+    if out is None:
+        out = empty_matrix(n, k, dtype or torch.float32, dY.device)
+    if dbias is None:
+        dbias = torch.empty(n, dtype=torch.float32, device=dY.device)
+    code = _act_code(x_act)
+    x, x8 = _split(X)
+    my = mat(dY)
+    with _Device(dY, X, out, dbias) as d:
+        ws, nws = d.workspace(lib.mao_linear_backward_weight_workspace_size(
+            rows, k, n, my.dtype, 1 if x8 is not None or code else 0))
+        _check(lib.mao_linear_backward_weight(my, x, x8, code, mat(out),
+                                              _floats(dbias, n, "dbias"), 1 if accumulate else 0,
+                                              ws, nws, d.stream), "mao_linear_backward_weight")
+    return out, dbias
 
 
 def _as_batch(X):

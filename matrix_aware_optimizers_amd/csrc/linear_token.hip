@@ -1,0 +1,193 @@
+// The linear layer's forward product for a few rows (decoded tokens, short
+// prompts): y = act(x W^T + b) + res with up to 64 rows of x.
+//
+// Bound: reading W once. A workgroup takes 16 rows of W and all of K; its
+// wavefronts take 256-byte blocks of those rows in turn, straight from memory
+// into registers in the MFMA operand layout (16 x 16 results: W rows x tokens,
+// so a wavefront's load is 64 contiguous bytes of each of 16 rows), the next
+// block requested before the current one is multiplied. x is small and comes
+// from L2. The wavefronts' sums are joined through LDS in a fixed order and the
+// first wavefronts finish the result.
+#include "act.hpp"
+#include "layers.hpp"
+
+#include <algorithm>
+
+namespace mao {
+
+namespace {
+
+constexpr int kStep = 64;      // bytes of a row per MFMA step
+constexpr int kSteps = 4;      // steps per block
+constexpr int kBlockBytes = kStep * kSteps;
+
+template <typename T, int FT>
+__device__ __forceinline__ void mma16(const uint4& w, const uint4 (&x)[FT], f32x4_t (&acc)[FT]) {
+#pragma unroll
+  for (int f = 0; f < FT; ++f) {
+    if constexpr (sizeof(T) == 2) {
+      acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w),
+                                                       __builtin_bit_cast(bf16x8_t, x[f]), acc[f],
+                                                       0, 0, 0);
+    } else {
+      const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+      const uint32_t b[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        acc[f] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[e]), __uint_as_float(b[e]),
+                                                      acc[f], 0, 0, 0);
+    }
+  }
+}
+
+// 16 bytes of a row from element k, zero from K on
+template <typename T>
+__device__ __forceinline__ uint4 load_masked(const T* row, int k, int K) {
+  constexpr int EPC = 16 / (int)sizeof(T);
+  union {
+    uint4 v;
+    T e[EPC];
+  } u;
+  u.v = make_uint4(0, 0, 0, 0);
+  if (k + EPC <= K) {
+    u.v = *(const uint4*)(row + k);
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPC; ++i)
+      if (k + i < K) u.e[i] = row[k + i];
+  }
+  return u.v;
+}
+
+template <typename T, int FT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void linear_token_kernel(LinProblem P) {
+  constexpr int EPC = 16 / (int)sizeof(T), KSTEP = kStep / (int)sizeof(T);
+  constexpr int KBLK = KSTEP * kSteps;
+  __shared__ __attribute__((aligned(16))) float red[WAVES][FT][256];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int r = lane & 15, q = lane >> 4;
+  const int n0 = blockIdx.x * 16;
+  const T* wrow = (const T*)P.B + (int64_t)min(n0 + r, P.N - 1) * P.ldb;
+  const T* xrow[FT];
+#pragma unroll
+  for (int f = 0; f < FT; ++f)
+    xrow[f] = (const T*)P.A + (int64_t)min(16 * f + r, P.M - 1) * P.lda;
+  f32x4_t acc[FT];
+#pragma unroll
+  for (int f = 0; f < FT; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  uint4 w[2][kSteps], x[2][kSteps][FT];
+  auto load = [&](int b, int s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int k = b * KBLK + i * KSTEP + q * EPC;
+      w[s][i] = *(const uint4*)(wrow + k);
+#pragma unroll
+      for (int f = 0; f < FT; ++f) x[s][i][f] = *(const uint4*)(xrow[f] + k);
+    }
+  };
+  const int nb = P.K / KBLK;
+  int b = wave;
+  if (b < nb) load(b, 0);
+  while (b < nb) {
+    if (b + WAVES < nb) load(b + WAVES, 1);
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) mma16<T, FT>(w[0][i], x[0][i], acc);
+    b += WAVES;
+    if (b >= nb) break;
+    if (b + WAVES < nb) load(b + WAVES, 0);
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) mma16<T, FT>(w[1][i], x[1][i], acc);
+    b += WAVES;
+  }
+  // steps past the last whole block, one per wavefront in turn
+  const int k1 = nb * KBLK;
+  for (int t = wave; k1 + t * KSTEP < P.K; t += WAVES) {
+    const int k = k1 + t * KSTEP + q * EPC;
+    const uint4 wv = load_masked(wrow, k, P.K);
+    uint4 xv[FT];
+#pragma unroll
+    for (int f = 0; f < FT; ++f) xv[f] = load_masked(xrow[f], k, P.K);
+    mma16<T, FT>(wv, xv, acc);
+  }
+#pragma unroll
+  for (int f = 0; f < FT; ++f)
+    *(float4*)&red[wave][f][lane * 4] = make_float4(acc[f][0], acc[f][1], acc[f][2], acc[f][3]);
+  __syncthreads();
+  // thread (f, lane'): columns n0 + 4 (lane' / 16) + 0..3 of row 16 f + lane' % 16
+  for (int u = threadIdx.x; u < FT * 64; u += 64 * WAVES) {
+    const int f = u >> 6, l = u & 63;
+    const int row = 16 * f + (l & 15), col = n0 + 4 * (l >> 4);
+    if (row >= P.M || col >= P.N) continue;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < WAVES; ++k) {
+      const float4 t = *(const float4*)&red[k][f][l * 4];
+      v[0] += t.x;
+      v[1] += t.y;
+      v[2] += t.z;
+      v[3] += t.w;
+    }
+    const LinEpilogue& e = P.e;
+    const int n = min(4, P.N - col);
+    auto put = [&](void* p, int dtype, int64_t off) {
+      if (dtype == MAO_BF16) {
+        bf16_t* d = (bf16_t*)p + off;
+        if (n == 4) {
+          *(uint2*)d = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < n) d[i] = f32_to_bf16(v[i]);
+        }
+      } else {
+        float* d = (float*)p + off;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < n) d[i] = v[i];
+      }
+    };
+    if (e.bias) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < n) v[i] += load1_any(e.bias, e.bias_dtype, col + i);
+    }
+    if (e.z_out) put(e.z_out, e.zo_dtype, (int64_t)row * e.ldzo + col);
+    act_apply(e.act, v);
+    if (e.add) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < n) v[i] += load1_any(e.add, e.add_dtype, (int64_t)row * e.ldadd + col + i);
+    }
+    put(e.D, e.d_dtype, (int64_t)row * e.ldd + col);
+  }
+}
+
+template <typename T, int FT>
+mao_status go(const LinProblem& p, hipStream_t s) {
+  const dim3 grid((int)ceil_div(p.N, 16));
+  // wavefronts per workgroup: about three blocks of K each
+  const int64_t blocks = p.K / (kBlockBytes / (int)sizeof(T));
+  constexpr int WIDE = FT == 1 ? 16 : 8;  // more tokens need more registers
+  if (blocks >= 24)
+    hipLaunchKernelGGL((linear_token_kernel<T, FT, WIDE>), grid, dim3(64 * WIDE), 0, s, p);
+  else
+    hipLaunchKernelGGL((linear_token_kernel<T, FT, 4>), grid, dim3(256), 0, s, p);
+  MAO_LAUNCH_CHECK();
+  return MAO_OK;
+}
+
+template <typename T>
+mao_status pick(const LinProblem& p, hipStream_t s) {
+  if (p.M <= 16) return go<T, 1>(p, s);
+  if (p.M <= 32) return go<T, 2>(p, s);
+  return go<T, 4>(p, s);
+}
+
+}  // namespace
+
+mao_status launch_linear_token(int dtype, const LinProblem& p, hipStream_t s) {
+  return dtype == MAO_BF16 ? pick<bf16_t>(p, s) : pick<float>(p, s);
+}
+
+}  // namespace mao
