@@ -495,65 +495,60 @@ def q8_empty(rows, cols, fmt="int8", device=None) -> Q8:
     return Q8(codes[:, :cols], torch.empty((rows, blocks), dtype=torch.uint8, device=device))
 
 
-class _Device:
-    """The tensors' common device as current, its stream, and a workspace."""
-
-    def __init__(self, first, *rest):
-        torch = _torch()
-        dev = first.device
-        if dev.type != "cuda":
-            raise ValueError(f"tensors must be on the GPU, not on {dev}")
-        for t in rest:
-            if t is not None and t.device != dev:
-                raise ValueError(f"tensors on {dev} and {t.device}")
-        self.device = dev
-        self.guard = None
-        if dev.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        self.handle = _torch().cuda.current_stream(self.device).cuda_stream
-        self.stream = c_void_p(self.handle)
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
-
-    def workspace(self, nbytes):
-        """(pointer, bytes) of a buffer that only this stream's calls share. Under
-        graph capture it is the graph's own, so that a later, larger call
-        cannot take it away from the graph."""
-        if nbytes == 0:
-            return None, 0
-        if _torch().cuda.is_current_stream_capturing():
-            self.buf = _torch().empty(nbytes, dtype=_torch().uint8, device=self.device)
-            return c_void_p(self.buf.data_ptr()), nbytes
-        key = (self.device.index, self.handle)
-        buf = _layer_ws.get(key)
-        if buf is None or buf.numel() < nbytes:
-            buf = _torch().empty(nbytes, dtype=_torch().uint8, device=self.device)
-            _layer_ws[key] = buf
-        return c_void_p(buf.data_ptr()), buf.numel()
-
+# These calls are made per layer and, decoding, per token: the binding keeps to
+# one look at each tensor and caches what depends on sizes alone.
 
 _layer_ws: dict = {}
+_codes: dict = {}
+
+
+def _setup():
+    torch = _torch()
+    _codes[torch.float32] = F32
+    _codes[torch.bfloat16] = BF16
+    # the current device and stream as numbers, without building objects
+    global _get_device, _get_stream
+    _get_device = torch._C._cuda_getDevice
+    _get_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _mat(t) -> Mat:
+    """mat() for the calls below: one row may have any row stride."""
+    try:
+        rows, cols = t.shape
+        ld, unit = t.stride()
+    except ValueError:
+        raise ValueError("expected a 2-D row-major tensor (unit column stride)") from None
+    if unit != 1 and cols != 1:
+        raise ValueError("expected a 2-D row-major tensor (unit column stride)")
+    if rows == 1:
+        ld = (cols + 7) & ~7
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return Mat(t.data_ptr(), rows, cols, ld, code)
 
 
 def _matp(t):
-    return None if t is None else ctypes.byref(mat(t))
+    return None if t is None else ctypes.byref(_mat(t))
+
+
+def _new(rows, cols, dtype, device):
+    if cols % 8:
+        return empty_matrix(rows, cols, dtype, device)
+    return _torch().empty((rows, cols), dtype=dtype, device=device)
 
 
 def _vec(t, n, name):
-    """(pointer, dtype code) of an optional contiguous vector of n values."""
+    """(address, dtype code) of an optional contiguous vector of n values."""
     if t is None:
         return None, F32
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of {n} values")
-    return c_void_p(t.data_ptr()), dtype_code(t)
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype} of {name}")
+    return t.data_ptr(), code
 
 
 def _floats(t, n, name):
@@ -574,101 +569,156 @@ def _split(x):
     return _matp(x), None
 
 
+def _device(first, *rest):
+    """The device all tensors are on (entry points take one device's tensors)."""
+    if not _codes:
+        _setup()
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on the GPU, not on {dev}")
+    for t in rest:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    return dev
+
+
+def _workspace(nbytes, dev, stream):
+    """(address, bytes) of a buffer that only this stream's calls share, and the
+    object that keeps it. Under graph capture it is the graph's own, so that a
+    later, larger call cannot take it away from the graph."""
+    if nbytes == 0:
+        return None, 0, None
+    torch = _torch()
+    if torch.cuda.is_current_stream_capturing():
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return buf.data_ptr(), nbytes, buf
+    key = (dev.index, stream)
+    buf = _layer_ws.get(key)
+    if buf is None or buf.numel() < nbytes:
+        buf = _layer_ws[key] = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return buf.data_ptr(), buf.numel(), buf
+
+
+_sizes: dict = {}
+
+
+def _ws_bytes(name, *args):
+    key = (name, args)
+    n = _sizes.get(key)
+    if n is None:
+        n = _sizes[key] = getattr(load(), name)(*args)
+        if len(_sizes) > 4096:  # lengths that keep changing
+            _sizes.clear()
+    return n
+
+
+def _call(name, dev, args, nbytes=None):
+    """Runs an entry point on dev's current stream; with ``nbytes``, a workspace
+    of that size goes in front of the stream."""
+    if _get_device() != dev.index:
+        with _torch().cuda.device(dev):
+            return _call(name, dev, args, nbytes)
+    stream = _get_stream(dev.index)
+    fn = getattr(_lib or load(), name)
+    if nbytes is None:
+        status = fn(*args, stream)
+    else:
+        ws, have, keep = _workspace(nbytes, dev, stream)
+        status = fn(*args, ws, have, stream)
+        del keep
+    if status:
+        _check(status, name)
+
+
 def q8_quantize(X, fmt="int8", out=None) -> Q8:
     """Keeps X (bf16 or fp32) in 8 bits."""
+    dev = _device(X, out)
     if out is None:
-        out = q8_empty(X.shape[0], X.shape[1], fmt, X.device)
-    with _Device(X, out) as d:
-        _check(load().mao_q8_quantize(mat(X), ctypes.byref(out.c), d.stream), "mao_q8_quantize")
+        out = q8_empty(X.shape[0], X.shape[1], fmt, dev)
+    _call("mao_q8_quantize", dev, (_mat(X), ctypes.byref(out.c)))
     return out
 
 
 def q8_dequantize(q: Q8, act="none", dtype=None, out=None):
     """act(q) as a tensor (bf16 unless ``dtype`` or ``out`` says fp32)."""
+    dev = _device(q, out)
     if out is None:
-        out = empty_matrix(q.shape[0], q.shape[1], dtype or _torch().bfloat16, q.device)
-    with _Device(q, out) as d:
-        _check(load().mao_q8_dequantize(ctypes.byref(q.c), _act_code(act), mat(out), d.stream),
-               "mao_q8_dequantize")
+        out = _new(q.shape[0], q.shape[1], dtype or _torch().bfloat16, dev)
+    _call("mao_q8_dequantize", dev, (ctypes.byref(q.c), _act_code(act), _mat(out)))
     return out
 
 
 def layer_norm(X, gamma=None, beta=None, *, eps=1e-5, out=None, stats=True):
     """(Y, mean, rstd) of layer norm over the rows of X; the statistics are None
     without ``stats``."""
-    torch = _torch()
-    rows, cols = X.shape
+    dev = _device(X, gamma, beta, out)
+    x = _mat(X)
+    rows, cols = x.rows, x.cols
     if out is None:
-        out = empty_matrix(rows, cols, X.dtype, X.device)
+        out = _new(rows, cols, X.dtype, dev)
     mean = rstd = None
     if stats:
-        mean = torch.empty(rows, dtype=torch.float32, device=X.device)
-        rstd = torch.empty(rows, dtype=torch.float32, device=X.device)
+        torch = _torch()
+        mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=dev).unbind(0)
     g, gd = _vec(gamma, cols, "gamma")
     b, bd = _vec(beta, cols, "beta")
     if g is not None and b is not None and gd != bd:
         raise TypeError("gamma and beta must share a dtype")
-    with _Device(X, gamma, beta, out) as d:
-        _check(load().mao_layer_norm(mat(X), g, b, gd if g is not None else bd, eps, mat(out),
-                                     _ptr(mean), _ptr(rstd), d.stream), "mao_layer_norm")
+    _call("mao_layer_norm", dev,
+          (x, g, b, gd if g is not None else bd, eps, _mat(out),
+           mean.data_ptr() if stats else None, rstd.data_ptr() if stats else None))
     return out, mean, rstd
 
 
 def layer_norm_backward(dY, X, gamma, mean, rstd, *, add=None, out=None, dgamma=None, dbeta=None):
     """(dX, dgamma, dbeta) of layer_norm. X: its input, or the input's Q8
     checkpoint. ``add`` joins dX (the skip connection's gradient)."""
-    torch = _torch()
-    lib = load()
-    rows, cols = dY.shape
+    dev = _device(dY, X, gamma, mean, rstd, add, out, dgamma, dbeta)
+    dy = _mat(dY)
+    rows, cols = dy.rows, dy.cols
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd of the forward pass are needed")
     if out is None:
-        out = empty_matrix(rows, cols, dY.dtype, dY.device)
+        out = _new(rows, cols, dY.dtype, dev)
+    torch = _torch()
     if dgamma is None:
-        dgamma = torch.empty(cols, dtype=torch.float32, device=dY.device)
+        dgamma = torch.empty(cols, dtype=torch.float32, device=dev)
     if dbeta is None:
-        dbeta = torch.empty(cols, dtype=torch.float32, device=dY.device)
+        dbeta = torch.empty(cols, dtype=torch.float32, device=dev)
     g, gd = _vec(gamma, cols, "gamma")
     x, x8 = _split(X)
-    with _Device(dY, X, gamma, mean, rstd, add, out, dgamma, dbeta) as d:
-        ws, nws = d.workspace(lib.mao_layer_norm_backward_workspace_size(rows, cols))
-        _check(lib.mao_layer_norm_backward(
-            mat(dY), x, x8, g, gd, _floats(mean, rows, "mean"), _floats(rstd, rows, "rstd"),
-            _matp(add), mat(out), _floats(dgamma, cols, "dgamma"), _floats(dbeta, cols, "dbeta"),
-            ws, nws, d.stream), "mao_layer_norm_backward")
+    _call("mao_layer_norm_backward", dev,
+          (dy, x, x8, g, gd, _floats(mean, rows, "mean"), _floats(rstd, rows, "rstd"), _matp(add),
+           _mat(out), _floats(dgamma, cols, "dgamma"), _floats(dbeta, cols, "dbeta")),
+          _ws_bytes("mao_layer_norm_backward_workspace_size", rows, cols))
     return out, dgamma, dbeta
 
 
 def linear(X, W, bias=None, *, act="none", residual=None, out=None, preact=None):
     """act(X W^T + bias) + residual. ``preact``: a tensor that receives the value
     before the activation; ``out`` may be ``residual``."""
-    lib = load()
-    rows, k = X.shape
-    n = W.shape[0]
+    dev = _device(X, W, bias, residual, out, preact)
+    x, w = _mat(X), _mat(W)
     if out is None:
-        out = empty_matrix(rows, n, X.dtype, X.device)
-    b, bd = _vec(bias, n, "bias")
-    mx = mat(X)
-    with _Device(X, W, bias, residual, out, preact) as d:
-        ws, nws = d.workspace(lib.mao_linear_workspace_size(rows, k, n, mx.dtype))
-        _check(lib.mao_linear(mx, mat(W), b, bd, _act_code(act), _matp(residual), mat(out),
-                              _matp(preact), ws, nws, d.stream), "mao_linear")
+        out = _new(x.rows, w.rows, X.dtype, dev)
+    b, bd = _vec(bias, w.rows, "bias")
+    _call("mao_linear", dev,
+          (x, w, b, bd, _act_code(act), _matp(residual), _mat(out), _matp(preact)),
+          _ws_bytes("mao_linear_workspace_size", x.rows, x.cols, w.rows, x.dtype))
     return out
 
 
 def linear_backward_input(dY, W, *, act="none", preact=None, add=None, out=None):
     """(dY W) * act'(preact) + add: the gradient of the layer's input, taken back
     through the activation that made it. ``preact``: a tensor or a Q8."""
-    lib = load()
-    rows, n = dY.shape
-    k = W.shape[1]
+    dev = _device(dY, W, preact, add, out)
+    dy, w = _mat(dY), _mat(W)
     if out is None:
-        out = empty_matrix(rows, k, dY.dtype, dY.device)
-    code = _act_code(act)
+        out = _new(dy.rows, w.cols, dY.dtype, dev)
     z, z8 = _split(preact)
-    my = mat(dY)
-    with _Device(dY, W, preact, add, out) as d:
-        ws, nws = d.workspace(lib.mao_linear_backward_input_workspace_size(rows, k, n, my.dtype))
-        _check(lib.mao_linear_backward_input(my, mat(W), code, z, z8, _matp(add), mat(out), ws, nws,
-                                             d.stream), "mao_linear_backward_input")
+    _call("mao_linear_backward_input", dev,
+          (dy, w, _act_code(act), z, z8, _matp(add), _mat(out)),
+          _ws_bytes("mao_linear_backward_input_workspace_size", dy.rows, w.cols, w.rows, dy.dtype))
     return out
 
 
@@ -677,25 +727,22 @@ def linear_backward_weight(dY, X, *, x_act="none", dtype=None, out=None, dbias=N
     """(dW, dbias) = (dY^T x_act(X), column sums of dY). X: the layer's input or
     its Q8 checkpoint. With ``accumulate`` both are added to ``out`` and
     ``dbias``, which then have to be given."""
-    torch = _torch()
-    lib = load()
-    rows, n = dY.shape
-    k = X.shape[1]
+    dev = _device(dY, X, out, dbias)
     if accumulate and (out is None or dbias is None):
         raise ValueError("accumulate needs out and dbias")
+    torch = _torch()
+    dy = _mat(dY)
+    rows, n, k = dy.rows, dy.cols, X.shape[1]
     if out is None:
-        out = empty_matrix(n, k, dtype or torch.float32, dY.device)
+        out = _new(n, k, dtype or torch.float32, dev)
     if dbias is None:
-        dbias = torch.empty(n, dtype=torch.float32, device=dY.device)
+        dbias = torch.empty(n, dtype=torch.float32, device=dev)
     code = _act_code(x_act)
     x, x8 = _split(X)
-    my = mat(dY)
-    with _Device(dY, X, out, dbias) as d:
-        ws, nws = d.workspace(lib.mao_linear_backward_weight_workspace_size(
-            rows, k, n, my.dtype, 1 if x8 is not None or code else 0))
-        _check(lib.mao_linear_backward_weight(my, x, x8, code, mat(out),
-                                              _floats(dbias, n, "dbias"), 1 if accumulate else 0,
-                                              ws, nws, d.stream), "mao_linear_backward_weight")
+    _call("mao_linear_backward_weight", dev,
+          (dy, x, x8, code, _mat(out), _floats(dbias, n, "dbias"), 1 if accumulate else 0),
+          _ws_bytes("mao_linear_backward_weight_workspace_size", rows, k, n, dy.dtype,
+                    1 if x8 is not None or code else 0))
     return out, dbias
 
 

@@ -169,7 +169,7 @@ struct LinProblem {
   int a_km, b_km;
   LinEpilogue e;
 };
-size_t lin_workspace(int dtype, int64_t M, int64_t N, int64_t K, int a_km, int b_km);
+size_t lin_workspace(int dtype, int64_t M, int64_t N, int64_t K);
 mao_status launch_linear(int dtype, const LinProblem& p, void* ws, hipStream_t s);
 
 // Up to kTokenRows rows of X against W (N x K), both K-contiguous.
