@@ -62,6 +62,27 @@ __device__ __forceinline__ float group_total(float v, float* buf) {
   return t;
 }
 
+// Two sums behind one barrier; buf alternates between two arrays from one call
+// to the next, so the barrier of the call between them separates its reads from
+// the next writes.
+template <int TPR>
+__device__ __forceinline__ void group_total2(float& a, float& b, float2* buf) {
+  a = wave_total(a);
+  b = wave_total(b);
+  if constexpr (TPR > 64) {
+    const int w = threadIdx.x >> 6, w0 = w / (TPR / 64) * (TPR / 64);
+    if ((threadIdx.x & 63) == 0) buf[w] = make_float2(a, b);
+    __syncthreads();
+    a = b = 0.f;
+#pragma unroll
+    for (int i = 0; i < TPR / 64; ++i) {
+      const float2 t = buf[w0 + i];
+      a += t.x;
+      b += t.y;
+    }
+  }
+}
+
 // Column runs past the row read as zero; so do the columns of a partial last
 // run that lie past the row (its storage is read whole: 16-byte aligned runs).
 __device__ __forceinline__ void mask8(float (&v)[8], int valid) {
@@ -92,7 +113,7 @@ __global__ __launch_bounds__(BLK) void norm_fwd_kernel(NormFwdArgs a) {
   const int nch = (a.cols + 7) >> 3;
   const bool ragged = (a.cols & 7) != 0;
   const float inv_n = 1.f / (float)a.cols;
-  constexpr bool PRE = TPR < 1024;  // parameters stay in registers
+  constexpr bool PRE = TPR < 1024 || V == 1;  // parameters stay in registers
   float gam[PRE ? V : 1][8], bet[PRE ? V : 1][8];
   if constexpr (PRE) {
 #pragma unroll
@@ -214,12 +235,12 @@ template <typename TDy, int XK, int TPR, int V, int BLK>
 __global__ __launch_bounds__(BLK) void norm_bwd_kernel(NormBwdArgs a) {
   constexpr int RPB = BLK / TPR;
   constexpr int kJoin = RPB > 1 ? 8 * V * TPR : 1;
-  __shared__ float red[2][BLK / 64];
+  __shared__ float2 red[2][BLK / 64];
   __shared__ float join[kJoin];
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   const int nch = (a.cols + 7) >> 3;
   const float inv_n = 1.f / (float)a.cols;
-  constexpr bool PRE = TPR < 1024;  // parameters stay in registers
+  constexpr bool PRE = TPR < 1024 || V == 1;  // parameters stay in registers
   float gam[PRE ? V : 1][8];
   if constexpr (PRE) {
 #pragma unroll
@@ -273,7 +294,7 @@ __global__ __launch_bounds__(BLK) void norm_bwd_kernel(NormBwdArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) g[i] = dy[i] * (PRE ? gam[PRE ? v : 0][i] : gl[i]);
   };
-  auto handle = [&](Row& q, int row) __attribute__((always_inline)) {
+  auto handle = [&](Row& q, int row, float2* buf) __attribute__((always_inline)) {
     const bool live = row < a.rows;
     const int lim = live ? a.cols : 0;
     float s0 = 0.f, s1 = 0.f;
@@ -289,8 +310,8 @@ __global__ __launch_bounds__(BLK) void norm_bwd_kernel(NormBwdArgs a) {
         s1 += g[i] * xh[i];
       }
     }
-    const float c0 = group_total<TPR>(s0, red[0]) * inv_n;
-    const float c1 = group_total<TPR>(s1, red[1]) * inv_n;
+    group_total2<TPR>(s0, s1, buf);
+    const float c0 = s0 * inv_n, c1 = s1 * inv_n;
     if (!live) return;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -313,11 +334,11 @@ __global__ __launch_bounds__(BLK) void norm_bwd_kernel(NormBwdArgs a) {
   };
   int r0 = blockIdx.x * RPB;
   // every thread of the block runs the same number of rounds (barriers inside)
-  if constexpr (TPR == 1024) {  // no registers for a second row
+  if constexpr (TPR == 1024 && V > 1) {  // no registers for a second row
     Row q;
-    for (; r0 < a.rows; r0 += step) {
+    for (int k = 0; r0 < a.rows; r0 += step, k ^= 1) {
       fetch(q, (int64_t)r0 + sub);
-      handle(q, r0 + sub);
+      handle(q, r0 + sub, red[k]);
     }
   } else {
     // two rows in turn: the next one is on its way while one is handled
@@ -325,11 +346,11 @@ __global__ __launch_bounds__(BLK) void norm_bwd_kernel(NormBwdArgs a) {
     fetch(q0, (int64_t)r0 + sub);
     while (true) {
       if (r0 + step < a.rows) fetch(q1, (int64_t)r0 + step + sub);
-      handle(q0, r0 + sub);
+      handle(q0, r0 + sub, red[0]);
       r0 += step;
       if (r0 >= a.rows) break;
       if (r0 + step < a.rows) fetch(q0, (int64_t)r0 + step + sub);
-      handle(q1, r0 + sub);
+      handle(q1, r0 + sub, red[1]);
       r0 += step;
       if (r0 >= a.rows) break;
     }
@@ -372,7 +393,7 @@ __global__ __launch_bounds__(BLK) void norm_bwd_kernel(NormBwdArgs a) {
 
 // Threads per workgroup; the backward pass takes more, for fewer partial rows.
 constexpr int fwd_block(int tpr) { return tpr > 256 ? tpr : 256; }
-constexpr int bwd_block(int tpr) { return tpr > 512 ? tpr : 512; }
+constexpr int bwd_block(int tpr) { return tpr > 64 ? 1024 : 512; }
 
 template <typename TIn, int TPR, int V>
 mao_status fwd_launch(const NormFwdArgs& a, hipStream_t s) {
@@ -400,13 +421,14 @@ struct BwdShape {
   int tpr, v;
 };
 BwdShape bwd_shape(int64_t cols) {
-  // more than three runs (two for wide rows) do not fit the registers beside
-  // the column sums, two rows in flight and gamma
+  // A wavefront holds up to three runs per lane beside the column sums, two rows
+  // in flight and gamma; wider rows take one run per thread of a 1024-thread
+  // workgroup, which keeps 16 wavefronts on the CU (4093 x 4096 from 8 bits: two
+  // runs per thread and 8 wavefronts 26.7 us).
   if (cols <= 1536) return {64, (int)ceil_div(cols, 512)};
-  if (cols <= 2048) return {128, 2};
-  if (cols <= 4096) return {256, 2};
-  if (cols <= 8192) return {512, 2};
-  return {1024, cols <= 16384 ? 2 : 4};
+  if (cols <= 2048) return {256, 1};
+  if (cols <= 4096) return {512, 1};
+  return {1024, cols <= 8192 ? 1 : cols <= 16384 ? 2 : 4};
 }
 
 template <typename TDy, int XK, int TPR, int V>
@@ -426,10 +448,10 @@ mao_status bwd_pick(const NormBwdArgs& a, hipStream_t s) {
       if (b.v == 1) return bwd_launch<TDy, XK, 64, 1>(a, s);
       if (b.v == 2) return bwd_launch<TDy, XK, 64, 2>(a, s);
       return bwd_launch<TDy, XK, 64, 3>(a, s);
-    case 128: return bwd_launch<TDy, XK, 128, 2>(a, s);
-    case 256: return bwd_launch<TDy, XK, 256, 2>(a, s);
-    case 512: return bwd_launch<TDy, XK, 512, 2>(a, s);
+    case 256: return bwd_launch<TDy, XK, 256, 1>(a, s);
+    case 512: return bwd_launch<TDy, XK, 512, 1>(a, s);
     default:
+      if (b.v == 1) return bwd_launch<TDy, XK, 1024, 1>(a, s);
       if (b.v == 2) return bwd_launch<TDy, XK, 1024, 2>(a, s);
       return bwd_launch<TDy, XK, 1024, 4>(a, s);
   }

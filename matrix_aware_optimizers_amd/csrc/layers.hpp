@@ -123,11 +123,7 @@ enum { kXInt8 = 2, kXE4m3 = 3 };
 int norm_bwd_blocks(int64_t rows, int64_t cols);
 mao_status launch_norm_bwd(const NormBwdArgs& a, int dy_dtype, int x_kind, hipStream_t s);
 
-// ---- column sums (column_sum.hip) ----------------------------------------
-int column_sum_blocks(int64_t rows, int64_t cols);
-// out[j] (+)= sum_i x[i][j]; part: blocks * cols floats
-mao_status launch_column_sum(const void* x, int dtype, int64_t ldx, int rows, int cols,
-                             float* part, float* out, int accumulate, hipStream_t s);
+// ---- join of partial column sums (partial_sum.hip) ----------------------------------------
 // out0[j] (+)= sum_b part[b * stride + j]; out1 the same from part + off1. Either
 // may be nullptr.
 mao_status launch_partial_sum(const float* part, int64_t stride, int blocks, int cols, float* out0,
@@ -170,7 +166,10 @@ struct LinProblem {
   LinEpilogue e;
 };
 size_t lin_workspace(int dtype, int64_t M, int64_t N, int64_t K);
-mao_status launch_linear(int dtype, const LinProblem& p, void* ws, hipStream_t s);
+// sums (weight gradient, or nullptr): lin_sum_rows x M floats that receive
+// partial column sums of A.
+int lin_sum_rows(int dtype, int64_t M, int64_t N, int64_t K);
+mao_status launch_linear(int dtype, const LinProblem& p, void* ws, float* sums, hipStream_t s);
 
 // Up to kTokenRows rows of X against W (N x K), both K-contiguous.
 constexpr int kTokenRows = 64;

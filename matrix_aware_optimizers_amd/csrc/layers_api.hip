@@ -104,7 +104,7 @@ WeightWs carve_weight(void* base, int64_t rows, int64_t k, int64_t n, int dtype,
   w.ldx = ws_ld(k);
   if (rebuilt) w.x = c.take<char>((size_t)rows * w.ldx * dtype_size(dtype));
   w.part = c.take<char>(lin_workspace(dtype, n, k, rows));
-  w.sums = c.take<float>((size_t)column_sum_blocks(rows, n) * n);
+  w.sums = c.take<float>((size_t)lin_sum_rows(dtype, n, k, rows) * n);
   w.bytes = c.used;
   return w;
 }
@@ -314,7 +314,7 @@ mao_status mao_linear(mao_mat X, mao_mat W, const void* bias, int32_t bias_dtype
     p.e.add_dtype = residual->dtype;
   }
   if (X.rows <= kTokenRows) return launch_linear_token(X.dtype, p, (hipStream_t)stream);
-  return launch_linear(X.dtype, p, workspace, (hipStream_t)stream);
+  return launch_linear(X.dtype, p, workspace, nullptr, (hipStream_t)stream);
 }
 
 mao_status mao_linear_backward_input(mao_mat dY, mao_mat W, int32_t act, const mao_mat* Z,
@@ -372,7 +372,7 @@ mao_status mao_linear_backward_input(mao_mat dY, mao_mat W, int32_t act, const m
     p.e.ldadd = add->ld;
     p.e.add_dtype = add->dtype;
   }
-  return launch_linear(dY.dtype, p, workspace, (hipStream_t)stream);
+  return launch_linear(dY.dtype, p, workspace, nullptr, (hipStream_t)stream);
 }
 
 mao_status mao_linear_backward_weight(mao_mat dY, const mao_mat* X, const mao_q8* X8,
@@ -428,10 +428,10 @@ mao_status mao_linear_backward_weight(mao_mat dY, const mao_mat* X, const mao_q8
     p.e.ldadd = dW.ld;
     p.e.add_dtype = dW.dtype;
   }
-  MAO_TRY(launch_linear(dY.dtype, p, w.part, s));
+  MAO_TRY(launch_linear(dY.dtype, p, w.part, dbias ? w.sums : nullptr, s));
   if (dbias)
-    MAO_TRY(launch_column_sum(dY.data, dY.dtype, dY.ld, (int)dY.rows, (int)dY.cols, w.sums, dbias,
-                              accumulate != 0, s));
+    MAO_TRY(launch_partial_sum(w.sums, p.M, lin_sum_rows(dY.dtype, p.M, p.N, p.K), p.M, dbias,
+                               nullptr, 0, accumulate != 0, s));
   return MAO_OK;
 }
 

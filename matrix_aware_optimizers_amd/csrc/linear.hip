@@ -22,7 +22,7 @@ constexpr int kSlots = 512;  // workgroups resident at once: two per CU
 // partial tiles (written and read once) and a launch. Rates of the estimate
 // (bf16: 16384 x 6144 x 1536 and 6144 x 1536 x 16384 on MI355X): 128 x 192 and
 // 192 x 128 tiles 4.1 TFLOP/s per CU, 128 x 128 tiles 3.6 (they read 20% more
-// operand bytes per flop); fp32 0.5; partial tiles 4 TB/s; 3 us to start and end
+// operand bytes per flop); fp32 0.5; partial results 4 TB/s; 3 us to start and end
 // a workgroup, 4 us for the second launch.
 Plan make_plan(int dtype, bool mixed, int64_t M, int64_t N, int64_t K) {
   static const int shape[3][2] = {{128, 192}, {192, 128}, {128, 128}};
@@ -44,7 +44,7 @@ Plan make_plan(int dtype, bool mixed, int64_t M, int64_t N, int64_t K) {
       const int64_t wgs = tiles * s;
       const double alone = wgs <= kSlots / 2 ? 1.0 / 1.7 : 1.0;
       double us = (double)ceil_div(wgs, kSlots) * (ceil_div(slices, s) * slice_us * alone + 3.0);
-      if (s > 1) us += 4.0 + 8.0 * wgs * bm * bn / 4e6;
+      if (s > 1) us += 4.0 + 8.0 * s * M * N / 4e6;
       if (best_us == 0.0 || us < best_us) {
         best_us = us;
         best.cfg = c;
@@ -52,7 +52,7 @@ Plan make_plan(int dtype, bool mixed, int64_t M, int64_t N, int64_t K) {
         best.tiles_m = tm;
         best.tiles_n = tn;
         best.slices = slices;
-        best.ws = s > 1 ? (size_t)wgs * bm * bn * 4 : 0;
+        best.ws = s > 1 ? (size_t)s * M * round_up(N, 8) * 4 : 0;
       }
     }
   }
@@ -66,7 +66,12 @@ size_t lin_workspace(int dtype, int64_t M, int64_t N, int64_t K) {
   return std::max(make_plan(dtype, false, M, N, K).ws, make_plan(dtype, true, M, N, K).ws);
 }
 
-mao_status launch_linear(int dtype, const LinProblem& p, void* ws, hipStream_t s) {
+int lin_sum_rows(int dtype, int64_t M, int64_t N, int64_t K) {
+  const Plan pl = make_plan(dtype, false, M, N, K);
+  return (int)(pl.split * pl.tiles_n);
+}
+
+mao_status launch_linear(int dtype, const LinProblem& p, void* ws, float* sums, hipStream_t s) {
   // forward and input gradient: every tensor of the epilogue but a checkpoint is
   // bf16 (the weight gradient's kernels take either result type)
   const LinEpilogue& e = p.e;
@@ -76,14 +81,21 @@ mao_status launch_linear(int dtype, const LinProblem& p, void* ws, hipStream_t s
   LinArgs a = {};
   a.p = p;
   a.part = (float*)ws;
+  a.ldpart = round_up(p.N, 8);
+  a.sums = sums;
   a.tiles_m = (int)pl.tiles_m;
   a.tiles_n = (int)pl.tiles_n;
   a.tiles = (int)(pl.tiles_m * pl.tiles_n);
   a.split = pl.split;
   a.slices = (int)pl.slices;
-  if (!p.a_km && !p.b_km) return linear_forward_tiles(dtype, pl.cfg, bf, a, s);
-  if (!p.a_km && p.b_km) return linear_input_grad_tiles(dtype, pl.cfg, bf, a, s);
-  return linear_weight_grad_tiles(dtype, pl.cfg, bf, a, s);
+  const bool slope = !p.a_km && p.b_km;
+  if (!p.a_km && !p.b_km)
+    MAO_TRY(linear_forward_tiles(dtype, pl.cfg, bf, a, s));
+  else if (slope)
+    MAO_TRY(linear_input_grad_tiles(dtype, pl.cfg, bf, a, s));
+  else
+    MAO_TRY(linear_weight_grad_tiles(dtype, pl.cfg, bf, a, s));
+  return pl.split > 1 ? launch_linear_join(p, a.part, a.ldpart, pl.split, slope, s) : MAO_OK;
 }
 
 }  // namespace mao

@@ -7,9 +7,15 @@ namespace mao {
 
 struct LinArgs {
   LinProblem p;
-  float* part;   // partial tiles (split > 1)
+  float* part;     // fp32 partial results [split][M][ldpart] (split > 1)
+  int64_t ldpart;
+  float* sums;     // weight gradient: partial column sums of A [split * tiles_n][M], or nullptr
   int tiles_m, tiles_n, tiles, split, slices;
 };
+
+// Adds a.split partial results and finishes them (linear_join.hip).
+mao_status launch_linear_join(const LinProblem& p, const float* part, int64_t ldpart, int split,
+                              bool slope, hipStream_t s);
 
 // Tile configurations (linear_tile.hpp).
 enum { CFG_128x192 = 0, CFG_192x128 = 1, CFG_128x128 = 2 };

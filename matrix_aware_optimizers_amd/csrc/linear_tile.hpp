@@ -34,8 +34,8 @@
 // leave in one instruction.
 //
 // Few tiles: K is split over several workgroups per tile. Their fp32 partial
-// tiles go to the workspace, and a second launch adds them in a fixed order and
-// runs the same epilogue. No atomics anywhere.
+// results go to the workspace, and a second launch (linear_join.hip) adds them
+// in a fixed order and finishes the result. No atomics anywhere.
 #pragma once
 
 #include "act.hpp"
@@ -145,31 +145,29 @@ __device__ __forceinline__ void finish(const f32x16_t* acc, float* reg, const Li
   constexpr bool SLOPE = KIND == EPI_SLOPE && ACT != MAO_ACT_NONE;
   const int lane = threadIdx.x & 63;
   const bool q8 = SLOPE && e.z_kind > MAO_BF16;
-  RawT<BF> zr[SLOPE ? IT : 1], ar[IT];
-  int scale[SLOPE ? IT : 1];
-  if constexpr (SLOPE) {
-#pragma unroll
-    for (int it = 0; it < IT; ++it) {
-      const int idx = it * 64 + lane, row = row0 + idx / CPR, col = col0 + 8 * (idx % CPR);
-      if (row >= P.M || col >= P.N) continue;
+  struct Inputs {
+    RawT<BF> z, a;
+    int scale;
+  };
+  auto load = [&](int it, Inputs& t) __attribute__((always_inline)) {
+    const int idx = it * 64 + lane, row = row0 + idx / CPR, col = col0 + 8 * (idx % CPR);
+    if (row >= P.M || col >= P.N) return;
+    if constexpr (SLOPE) {
       const int64_t off = (int64_t)row * e.ldzi + col;
       if (q8) {
         const uint2 w = *(const uint2*)((const uint8_t*)e.z_in + off);
-        zr[it].a.x = w.x;
-        zr[it].a.y = w.y;
-        scale[it] = e.z_scales[(int64_t)row * e.ldzs + (col >> 5)];
+        t.z.a.x = w.x;
+        t.z.a.y = w.y;
+        t.scale = e.z_scales[(int64_t)row * e.ldzs + (col >> 5)];
       } else {
-        zr[it].load(e.z_in, e.z_kind, off);
+        t.z.load(e.z_in, e.z_kind, off);
       }
     }
-  }
-  if (e.add != nullptr) {
-#pragma unroll
-    for (int it = 0; it < IT; ++it) {
-      const int idx = it * 64 + lane, row = row0 + idx / CPR, col = col0 + 8 * (idx % CPR);
-      if (row < P.M && col < P.N) ar[it].load(e.add, e.add_dtype, (int64_t)row * e.ldadd + col);
-    }
-  }
+    if (e.add != nullptr) t.a.load(e.add, e.add_dtype, (int64_t)row * e.ldadd + col);
+  };
+  Inputs t0, t1;
+  load(0, t0);
+  load(1, t1);
   {
     float* d = reg + (lane & 31) * LD + 4 * (lane >> 5);
 #pragma unroll
@@ -180,13 +178,18 @@ __device__ __forceinline__ void finish(const f32x16_t* acc, float* reg, const Li
                                                      acc[j][4 * g + 2], acc[j][4 * g + 3]);
   }
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll
+  // rolled: most launches run this code once per workgroup, from a cold
+  // instruction cache
+#pragma unroll 1
   for (int it = 0; it < IT; ++it) {
     const int idx = it * 64 + lane, rr = idx / CPR, cc = 8 * (idx % CPR);
     const int row = row0 + rr, col = col0 + cc, valid = P.N - col;
     const float4 lo = *(const float4*)(reg + rr * LD + cc);
     const float4 hi = *(const float4*)(reg + rr * LD + cc + 4);
     float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    const Inputs t = t0;
+    t0 = t1;
+    if (it + 2 < IT) load(it + 2, t1);
     if (row >= P.M || valid <= 0) continue;
     if constexpr (KIND == EPI_FORWARD) {
       const float4 b0 = *(const float4*)(bias + cc), b1 = *(const float4*)(bias + cc + 4);
@@ -200,19 +203,19 @@ __device__ __forceinline__ void finish(const f32x16_t* acc, float* reg, const Li
     if constexpr (SLOPE) {
       float z[8];
       if (q8) {
-        const float s = q8_scale_value(scale[it]);
+        const float s = q8_scale_value(t.scale);
         const int fmt = e.z_kind == kXInt8 ? MAO_Q8_INT8 : MAO_Q8_E4M3;
-        q8_decode4_any(fmt, zr[it].a.x, s, z);
-        q8_decode4_any(fmt, zr[it].a.y, s, z + 4);
+        q8_decode4_any(fmt, t.z.a.x, s, z);
+        q8_decode4_any(fmt, t.z.a.y, s, z + 4);
       } else {
-        zr[it].get(e.z_kind, z);
+        t.z.get(e.z_kind, z);
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] *= act_slope<ACT>(z[k]);
     }
     if (e.add != nullptr) {
       float w[8];
-      ar[it].get(e.add_dtype, w);
+      t.a.get(e.add_dtype, w);
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] += w[k];
     }
@@ -501,9 +504,49 @@ __global__ __launch_bounds__(kThreads, C::OCC) void linear_tile_kernel(LinArgs a
   };
 
   uint4 fa[2][FM], fb[2][FN];
+  // Column sums of A (the bias gradient) on the way: slice g of the reduction is
+  // summed by the workgroup whose tile column is g modulo the number of tile
+  // columns, so every slice is summed once per tile row and the work is spread
+  // evenly. A thread adds one 16-byte chunk of every RS-th k row of the slice.
+  constexpr int ACH = C::BM * C::ES / 16, RS = kThreads / ACH, EPC = C::EPC;
+  constexpr bool SUMS = KIND == EPI_PLAIN;
+  float csum[SUMS ? EPC : 1];
+  if constexpr (SUMS)
+#pragma unroll
+    for (int i = 0; i < EPC; ++i) csum[i] = 0.f;
+  auto add_columns = [&](const unsigned char* st) __attribute__((always_inline)) {
+    const int c = (int)threadIdx.x % ACH, r0 = (int)threadIdx.x / ACH;
+    if (r0 >= RS) return;
+#pragma unroll
+    for (int r = 0; r < (C::KS + RS - 1) / RS; ++r) {
+      const int kr = r0 + r * RS;
+      if (C::KS % RS != 0 && kr >= C::KS) break;
+      const uint4 q = *(const uint4*)(st + kr * C::BM * C::ES + ((c ^ swz_m<C::BM, C::ES>(kr)) << 4));
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (C::ES == 2) {
+          csum[2 * i] += __uint_as_float(w[i] << 16);
+          csum[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
+        } else {
+          csum[i] += __uint_as_float(w[i]);
+        }
+      }
+    }
+  };
+  int next_sum = -1;  // this workgroup's next slice to sum, from s0
+  if constexpr (SUMS)
+    if (a.sums != nullptr) next_sum = (tn - s0 % a.tiles_n + a.tiles_n) % a.tiles_n;
+
   // slice k out of `cur`; `nxt` holds slice k + 1 (landing)
   auto step = [&](unsigned char* cur, const unsigned char* nxt, int k)
                   __attribute__((always_inline)) {
+    if constexpr (SUMS) {
+      if (k == next_sum) {
+        add_columns(cur);
+        next_sum += a.tiles_n;
+      }
+    }
 #pragma unroll
     for (int s = 0; s + 1 < SUB; ++s) {
       read(cur, s + 1, fa[(s + 1) & 1], fb[(s + 1) & 1]);
@@ -576,6 +619,8 @@ __global__ __launch_bounds__(kThreads, C::OCC) void linear_tile_kernel(LinArgs a
     oa.stage_tail(st0, A, P.lda, m0, P.M, k0, P.K);
     ob.stage_tail(st0 + C::AB, B, P.ldb, n0, P.N, k0, P.K);
     __syncthreads();
+    if constexpr (SUMS)
+      if (nk == next_sum) add_columns(st0);
 #pragma unroll 1
     for (int s = 0; s < SUB; ++s) {
       // s is a run-time value here: fragment offsets by select, one copy of code
@@ -588,6 +633,24 @@ __global__ __launch_bounds__(kThreads, C::OCC) void linear_tile_kernel(LinArgs a
     __syncthreads();
   }
 
+  if constexpr (SUMS) {
+    if (a.sums != nullptr) {  // join the RS row groups, in order
+      float* js = (float*)st0;
+      const int c = (int)threadIdx.x % ACH, r0 = (int)threadIdx.x / ACH;
+      if (r0 < RS)
+#pragma unroll
+        for (int i = 0; i < EPC; ++i) js[r0 * C::BM + c * EPC + i] = csum[i];
+      __syncthreads();
+      if (threadIdx.x < C::BM && m0 + (int)threadIdx.x < P.M) {
+        float t = 0.f;
+#pragma unroll
+        for (int r = 0; r < RS; ++r) t += js[r * C::BM + threadIdx.x];
+        a.sums[((int64_t)part * a.tiles_n + tn) * P.M + m0 + threadIdx.x] = t;
+      }
+      __syncthreads();
+    }
+  }
+
   // The accumulators stay in AGPRs and are read value by value: as ordinary
   // registers the exchanges below, which overwrite their operands, would have
   // them all copied first, and spilled.
@@ -596,18 +659,17 @@ __global__ __launch_bounds__(kThreads, C::OCC) void linear_tile_kernel(LinArgs a
 #pragma unroll
     for (int j = 0; j < FN; ++j) asm volatile("" : "+a"(acc[i][j]));
 
-  if (a.split > 1) {
-    float* w = a.part + ((int64_t)part * a.tiles + tile) * (C::BM * C::BN);
-    w += (int64_t)wave * (C::BM * C::BN / 4);
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j)
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          *(float4*)(w + (((i * FN + j) * 4 + g) * 64 + lane) * 4) =
-              make_float4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
-                          acc[i][j][4 * g + 3]);
+  float* reg = (float*)((wave < 2 ? st0 : st1) + (wave & 1) * C::PIECE);
+  const int row0 = m0 + wm * (C::BM / 2), col0 = n0 + wn * (C::BN / 2);
+  if (a.split > 1) {  // fp32 partial result, row-major like the result itself
+    LinProblem q;
+    q.M = P.M;
+    q.N = P.N;
+    q.e.D = a.part + (int64_t)part * P.M * a.ldpart;
+    q.e.ldd = a.ldpart;
+    q.e.d_dtype = MAO_F32;
+    q.e.add = nullptr;
+    finish_all<EPI_PLAIN, MAO_ACT_NONE, false, C::JU>(acc, reg, q, nullptr, row0, col0);
     return;
   }
   float* bias = (float*)(st1 + C::STAGE - C::BN * 4);
@@ -615,53 +677,7 @@ __global__ __launch_bounds__(kThreads, C::OCC) void linear_tile_kernel(LinArgs a
     if (threadIdx.x < C::BN) bias[threadIdx.x] = bias_v;
     __syncthreads();
   }
-  float* reg = (float*)((wave < 2 ? st0 : st1) + (wave & 1) * C::PIECE);
-  finish_any<KIND, BF, C::JU>(acc, reg, P, bias + wn * (C::BN / 2), m0 + wm * (C::BM / 2),
-                              n0 + wn * (C::BN / 2));
-}
-
-// Adds the partial tiles of a split launch and finishes them: one wavefront per
-// 32 x (32 JU) piece of a tile.
-template <typename C, EpiKind KIND, bool BF>
-__global__ __launch_bounds__(64) void linear_join_kernel(LinArgs a) {
-  constexpr int FM = C::FM, FN = C::FN, JU = C::JU, PER = FM * (FN / JU);
-  __shared__ __attribute__((aligned(16))) float reg[32 * piece_ld(JU)];
-  __shared__ __attribute__((aligned(16))) float bias[32 * JU];
-  const int tile = blockIdx.x / (4 * PER), u = blockIdx.x % (4 * PER);
-  const int wave = u / PER, i = u / (FN / JU) % FM, j = u % (FN / JU) * JU;
-  const int lane = threadIdx.x;
-  int tm, tn;
-  tile_of(a, tile, tm, tn);
-  const float* w = a.part + (int64_t)tile * (C::BM * C::BN) + (int64_t)wave * (C::BM * C::BN / 4);
-  f32x16_t acc[1][JU];
-#pragma unroll
-  for (int q = 0; q < JU; ++q)
-#pragma unroll
-    for (int v = 0; v < 16; ++v) acc[0][q][v] = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < a.split; ++s) {
-    const float* ws = w + (int64_t)s * a.tiles * (C::BM * C::BN);
-#pragma unroll
-    for (int q = 0; q < JU; ++q)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const float4 t = *(const float4*)(ws + (((i * FN + j + q) * 4 + g) * 64 + lane) * 4);
-        acc[0][q][4 * g] += t.x;
-        acc[0][q][4 * g + 1] += t.y;
-        acc[0][q][4 * g + 2] += t.z;
-        acc[0][q][4 * g + 3] += t.w;
-      }
-  }
-  const int wm = wave >> 1, wn = wave & 1;
-  const int row0 = tm * C::BM + wm * (C::BM / 2) + i * 32;
-  const int col0 = tn * C::BN + wn * (C::BN / 2) + j * 32;
-  if constexpr (KIND == EPI_FORWARD) {
-#pragma unroll
-    for (int q = 0; q < 32 * JU; q += 64)
-      if (q + lane < 32 * JU) bias[q + lane] = bias_at(a.p, col0 + q + lane);
-    __syncthreads();
-  }
-  finish_any<KIND, BF, JU>(acc, reg, a.p, bias, row0, col0);
+  finish_any<KIND, BF, C::JU>(acc, reg, P, bias + wn * (C::BN / 2), row0, col0);
 }
 
 template <typename C, EpiKind KIND, bool BF>
@@ -669,11 +685,6 @@ mao_status go(const LinArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((linear_tile_kernel<C, KIND, BF>), dim3(a.tiles * a.split), dim3(kThreads), 0, s,
                      a);
   MAO_LAUNCH_CHECK();
-  if (a.split > 1) {
-    constexpr int UNITS = 4 * C::FM * (C::FN / C::JU);
-    hipLaunchKernelGGL((linear_join_kernel<C, KIND, BF>), dim3(a.tiles * UNITS), dim3(64), 0, s, a);
-    MAO_LAUNCH_CHECK();
-  }
   return MAO_OK;
 }
 
