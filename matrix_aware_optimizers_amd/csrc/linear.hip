@@ -14,36 +14,50 @@ struct Plan {
   size_t ws;
 };
 
-constexpr int kSlots = 512;  // workgroups resident at once: two per CU
+// Tile shapes: workgroups per CU, TFLOP/s of a CU full of them (long K, bf16,
+// measured; [0] K-contiguous left operand, [1] both K-major) and the
+// microseconds a workgroup takes to start and to finish its result.
+struct Shape {
+  int bm, bn, per_cu;
+  double rate[2], ends;
+};
+const Shape kShapes[CFG_COUNT] = {
+    {256, 256, 1, {5.4, 5.15}, 12.0},
+    {256, 192, 1, {5.05, 4.57}, 10.0},
+    {128, 192, 2, {4.5, 4.65}, 10.0},
+    {192, 128, 2, {4.4, 4.5}, 10.0},
+    {128, 128, 2, {3.6, 3.6}, 7.0},
+};
+constexpr double kF32Rate = 0.5;  // of the 128 x 128 tile
 
-// The cut with the shortest estimated time. Two workgroups share a CU, so tiles
-// run in rounds of 512; a workgroup alone on its CU runs 1.7 times as fast. With few
-// tiles K is split: more workgroups, each part followed by one pass over the
-// partial tiles (written and read once) and a launch. Rates of the estimate
-// (bf16: 16384 x 6144 x 1536 and 6144 x 1536 x 16384 on MI355X): 128 x 192 and
-// 192 x 128 tiles 4.1 TFLOP/s per CU, 128 x 128 tiles 3.6 (they read 20% more
-// operand bytes per flop); fp32 0.5; partial results 4 TB/s; 3 us to start and end
-// a workgroup, 4 us for the second launch.
-Plan make_plan(int dtype, bool mixed, int64_t M, int64_t N, int64_t K) {
-  static const int shape[3][2] = {{128, 192}, {192, 128}, {128, 128}};
+// The cut with the shortest estimated time. Tiles run in rounds of 256 workgroups
+// times those that share a CU; a last round that is not full is shorter too (the
+// clock rises as CUs idle: 6144 x 1536 x 16384 in 144 tiles of 256 x 256 takes 0.85 of a
+// full round). A workgroup that has its CU to itself where two would fit runs
+// 1.7 times as fast. With few tiles K is split: more workgroups, then one pass over
+// the partial results (written and read at about 4 TB/s) and a launch.
+Plan make_plan(int dtype, bool mixed, bool km, int64_t M, int64_t N, int64_t K) {
   const int ks = dtype == MAO_BF16 ? 64 : 32;
   const int64_t slices = ceil_div(K, ks);
   Plan best = {};
   double best_us = 0.0;
-  for (int c = 0; c < 3; ++c) {
-    // fp32 operands and mixed result types come with the square tile only
+  for (int c = 0; c < CFG_COUNT; ++c) {
+    // fp32 operands and mixed result types come with the square small tile only
     if (c != CFG_128x128 && (dtype != MAO_BF16 || mixed)) continue;
-    const int bm = shape[c][0], bn = shape[c][1];
-    const int64_t tm = ceil_div(M, bm), tn = ceil_div(N, bn), tiles = tm * tn;
-    const double rate = (dtype != MAO_BF16 ? 0.5 : c == CFG_128x128 ? 3.6 : 4.1) * 0.5e6;
-    const double slice_us = 2.0 * bm * bn * ks / rate;
+    const Shape& h = kShapes[c];
+    const int64_t tm = ceil_div(M, h.bm), tn = ceil_div(N, h.bn), tiles = tm * tn;
+    const int64_t slots = 256 * h.per_cu;
+    const double rate = (dtype != MAO_BF16 ? kF32Rate : h.rate[km ? 1 : 0]) * 1e6 / h.per_cu;
+    const double slice_us = 2.0 * h.bm * h.bn * ks / rate;
     // parts of at least two slices, no more than 32, and only where a round is
     // not full without them
-    const int64_t most = tiles >= kSlots ? 1 : std::min<int64_t>({32, slices / 2, ceil_div(2 * kSlots, tiles)});
+    const int64_t most =
+        tiles >= slots ? 1 : std::min<int64_t>({32, slices / 2, ceil_div(2 * slots, tiles)});
     for (int64_t s = 1; s <= std::max<int64_t>(1, most); ++s) {
-      const int64_t wgs = tiles * s;
-      const double alone = wgs <= kSlots / 2 ? 1.0 / 1.7 : 1.0;
-      double us = (double)ceil_div(wgs, kSlots) * (ceil_div(slices, s) * slice_us * alone + 3.0);
+      const int64_t wgs = tiles * s, last = wgs % slots;
+      double one = ceil_div(slices, s) * slice_us;
+      if (h.per_cu > 1 && wgs <= 256) one /= 1.7;
+      double us = (one + h.ends) * ((double)(wgs / slots) + (last ? 0.65 + 0.35 * last / slots : 0.0));
       if (s > 1) us += 4.0 + 8.0 * s * M * N / 4e6;
       if (best_us == 0.0 || us < best_us) {
         best_us = us;
@@ -61,13 +75,13 @@ Plan make_plan(int dtype, bool mixed, int64_t M, int64_t N, int64_t K) {
 
 }  // namespace
 
-size_t lin_workspace(int dtype, int64_t M, int64_t N, int64_t K) {
+size_t lin_workspace(int dtype, bool km, int64_t M, int64_t N, int64_t K) {
   // the caller may not know the result types yet
-  return std::max(make_plan(dtype, false, M, N, K).ws, make_plan(dtype, true, M, N, K).ws);
+  return std::max(make_plan(dtype, false, km, M, N, K).ws, make_plan(dtype, true, km, M, N, K).ws);
 }
 
 int lin_sum_rows(int dtype, int64_t M, int64_t N, int64_t K) {
-  const Plan pl = make_plan(dtype, false, M, N, K);
+  const Plan pl = make_plan(dtype, false, true, M, N, K);
   return (int)(pl.split * pl.tiles_n);
 }
 
@@ -77,7 +91,7 @@ mao_status launch_linear(int dtype, const LinProblem& p, void* ws, float* sums, 
   const LinEpilogue& e = p.e;
   const bool bf = e.d_dtype == MAO_BF16 && (!e.z_out || e.zo_dtype == MAO_BF16) &&
                   (!e.add || e.add_dtype == MAO_BF16) && (!e.z_in || e.z_kind != MAO_F32);
-  const Plan pl = make_plan(dtype, !(p.a_km && p.b_km) && !bf, p.M, p.N, p.K);
+  const Plan pl = make_plan(dtype, !p.a_km && !bf, p.a_km != 0, p.M, p.N, p.K);
   LinArgs a = {};
   a.p = p;
   a.part = (float*)ws;

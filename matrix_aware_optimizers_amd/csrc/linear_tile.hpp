@@ -50,20 +50,33 @@ typedef __attribute__((address_space(3))) void lds_void_t;
 typedef __attribute__((address_space(1))) const void gbl_void_t;
 typedef short lds_v4i16_t __attribute__((ext_vector_type(4), address_space(3)));
 
-constexpr int kThreads = 256;
-
 // s_waitcnt with vmcnt(n) and lgkmcnt(0)
 template <int N>
 __device__ __forceinline__ void wait_slice() {
   __builtin_amdgcn_s_waitcnt((N & 0xf) | (0x7 << 4) | ((N >> 4) << 14));
 }
 
+// s_waitcnt with lgkmcnt(0) alone
+__device__ __forceinline__ void wait_lds() {
+  __builtin_amdgcn_s_waitcnt(0xf | (0x7 << 4) | (0x3 << 14));
+}
+
 // What the epilogue does beyond D = acc + add.
-enum EpiKind { EPI_PLAIN, EPI_FORWARD, EPI_SLOPE };
+// EPI_PARTIAL: fp32 partial results of a split product, which the join reads soon.
+enum EpiKind { EPI_PLAIN, EPI_FORWARD, EPI_SLOPE, EPI_PARTIAL };
+
+// A result line is written whole and not read again here: it should not push
+// operand panels out of the L2 (16384 x 6144 x 1536 with gelu and its
+// pre-activation kept 342 -> 330 us, 16384 x 1536 x 6144 271 -> 253 us).
+__device__ __forceinline__ void store_once(void* p, const uint4& v) {
+  typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
+  const u32x4_t t = {v.x, v.y, v.z, v.w};
+  __builtin_nontemporal_store(t, (u32x4_t*)p);
+}
 
 // Stores v[0 .. valid) (8 at most) at element off. A run cut by the last column
 // goes out element by element, in a loop (rare, and short code matters here).
-template <bool BF>
+template <bool BF, bool ONCE = true>
 __device__ __forceinline__ void put8(void* p, int dtype, int64_t off, const float (&v)[8],
                                      int valid) {
   if (BF || dtype == MAO_BF16) {
@@ -74,7 +87,7 @@ __device__ __forceinline__ void put8(void* p, int dtype, int64_t off, const floa
     k.w = pack_bf16x2(v[6], v[7]);
     bf16_t* d = (bf16_t*)p + off;
     if (valid >= 8) {
-      *(uint4*)d = k;
+      store_once(d, k);
     } else {
 #pragma unroll 1
       for (int i = 0; i < valid; ++i) {
@@ -88,8 +101,17 @@ __device__ __forceinline__ void put8(void* p, int dtype, int64_t off, const floa
   } else {
     float* d = (float*)p + off;
     if (valid >= 8) {
-      *(float4*)d = make_float4(v[0], v[1], v[2], v[3]);
-      *(float4*)(d + 4) = make_float4(v[4], v[5], v[6], v[7]);
+      const uint4 a = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                 __float_as_uint(v[2]), __float_as_uint(v[3]));
+      const uint4 b = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]),
+                                 __float_as_uint(v[6]), __float_as_uint(v[7]));
+      if constexpr (ONCE) {
+        store_once(d, a);
+        store_once(d + 4, b);
+      } else {
+        *(uint4*)d = a;
+        *(uint4*)(d + 4) = b;
+      }
     } else {
       float w[8];
 #pragma unroll
@@ -219,7 +241,7 @@ __device__ __forceinline__ void finish(const f32x16_t* acc, float* reg, const Li
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] += w[k];
     }
-    put8<BF>(e.D, e.d_dtype, (int64_t)row * e.ldd + col, v, valid);
+    put8<BF, KIND != EPI_PARTIAL>(e.D, e.d_dtype, (int64_t)row * e.ldd + col, v, valid);
   }
   // the next piece overwrites reg: this one's reads are done
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -274,20 +296,21 @@ __device__ __forceinline__ void tile_of(const LinArgs& a, int tile, int& tm, int
   tn = in / gsz;
 }
 
-template <typename TIn, bool AKM, bool BKM, int BM_, int BN_, int KSB_, int NST_, int OCC_>
+template <typename TIn, bool AKM, bool BKM, int BM_, int BN_, int WM_, int WN_, int KSB_, int NST_, int OCC_>
 struct Cfg {
   using T = TIn;
   static constexpr bool akm = AKM, bkm = BKM;
   static constexpr int BM = BM_, BN = BN_, KSB = KSB_, NST = NST_, OCC = OCC_;
+  static constexpr int WM = WM_, WN = WN_, WAVES = WM * WN, THREADS = 64 * WAVES;  // wavefront grid
   static constexpr int ES = (int)sizeof(TIn), EPC = 16 / ES, KS = KSB / ES, SUB = KSB / 32;
-  static constexpr int FM = BM / 64, FN = BN / 64;
+  static constexpr int FM = BM / (32 * WM), FN = BN / (32 * WN);
   static constexpr int AB = BM * KSB, BB = BN * KSB, STAGE = AB + BB;
-  static constexpr int LA = AB / 16 / kThreads, LB = BB / 16 / kThreads;
+  static constexpr int LA = AB / 16 / THREADS, LB = BB / 16 / THREADS;
   static constexpr int JU = FN % 2 == 0 ? 2 : FN;
   static constexpr int PIECE = 32 * piece_ld(JU) * 4;
-  static_assert(AB % (16 * kThreads) == 0 && BB % (16 * kThreads) == 0, "whole loads per thread");
+  static_assert(AB % (16 * THREADS) == 0 && BB % (16 * THREADS) == 0, "whole loads per thread");
   static_assert(NST >= 2 && NST <= 4, "ring stages");
-  static_assert(2 * PIECE + BN * 4 <= STAGE, "the epilogue's pieces and the bias fit the stages");
+  static_assert(WAVES / 2 * PIECE + BN * 4 <= STAGE, "the epilogue's pieces and the bias fit the stages");
 };
 
 // XOR permutation of a K-contiguous row's 16-byte chunks.
@@ -304,9 +327,9 @@ __device__ __forceinline__ int swz_m(int krow) {
 
 // Per-thread global sources of one operand's direct loads, and its LDS fragment
 // offsets.
-template <typename TIn, bool KM, int BX, int KSB, int NL>
+template <typename TIn, bool KM, int BX, int WX, int WAVES, int KSB, int NL>
 struct Operand {
-  static constexpr int ES = (int)sizeof(TIn), EPC = 16 / ES, F = BX / 64, SUB = KSB / 32;
+  static constexpr int ES = (int)sizeof(TIn), EPC = 16 / ES, F = BX / (32 * WX), SUB = KSB / 32;
   static constexpr int CPR = KM ? BX * ES / 16 : KSB / 16;  // chunks per LDS row
   const TIn* src[NL];
   int frag[KM ? F : SUB];
@@ -316,7 +339,7 @@ struct Operand {
     const int h = lane >> 5, r32 = lane & 31;
 #pragma unroll
     for (int q = 0; q < NL; ++q) {
-      const int L = (q * 4 + wave) * 64 + lane;
+      const int L = (q * WAVES + wave) * 64 + lane;
       const int r = L / CPR, slot = L % CPR;
       if constexpr (KM) {
         const int col = x0 + (slot ^ swz_m<BX, ES>(r)) * EPC;
@@ -326,7 +349,7 @@ struct Operand {
       }
     }
     if constexpr (!KM) {
-      const int r = w * (BX / 2) + r32;
+      const int r = w * (BX / WX) + r32;
 #pragma unroll
       for (int s = 0; s < SUB; ++s) frag[s] = r * KSB + (((2 * s + h) ^ swz_k<KSB>(r)) << 4);
     } else if constexpr (ES == 2) {
@@ -334,13 +357,13 @@ struct Operand {
       const int krow = 8 * h + (ti >> 2);
 #pragma unroll
       for (int f = 0; f < F; ++f) {
-        const int chunk = w * (BX / 16) + 4 * f + 2 * tg + ((ti >> 1) & 1);
+        const int chunk = w * (BX / (8 * WX)) + 4 * f + 2 * tg + ((ti >> 1) & 1);
         frag[f] = krow * BX * 2 + ((chunk ^ swz_m<BX, ES>(krow)) << 4) + 8 * (ti & 1);
       }
     } else {
 #pragma unroll
       for (int f = 0; f < F; ++f) {
-        const int col = w * (BX / 2) + 32 * f + r32;
+        const int col = w * (BX / WX) + 32 * f + r32;
         frag[f] = 4 * h * BX * 4 + (((col >> 2) ^ (h << 3)) << 4) + 4 * (col & 3);
       }
     }
@@ -352,7 +375,7 @@ struct Operand {
 #pragma unroll
     for (int q = 0; q < NL; ++q)
       __builtin_amdgcn_global_load_lds((gbl_void_t*)(src[q] + off),
-                                       (lds_void_t*)(st + (q * 4 + wave) * 1024), 16, 0, 0);
+                                       (lds_void_t*)(st + (q * WAVES + wave) * 1024), 16, 0, 0);
   }
   // partial slice [k0, kend): element by element, zero past kend
   __device__ __forceinline__ void stage_tail(unsigned char* st, const TIn* p, int64_t ld, int x0,
@@ -360,7 +383,7 @@ struct Operand {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll 1
     for (int q = 0; q < NL; ++q) {
-      const int L = (q * 4 + wave) * 64 + lane;
+      const int L = (q * WAVES + wave) * 64 + lane;
       const int r = L / CPR, slot = L % CPR;
       union {
         uint4 v;
@@ -406,7 +429,7 @@ __device__ __forceinline__ uint32_t u4e(const uint4& v, int e) {
 }
 
 template <typename C, EpiKind KIND, bool BF>
-__global__ __launch_bounds__(kThreads, C::OCC) void linear_tile_kernel(LinArgs a) {
+__global__ __launch_bounds__(C::THREADS, C::OCC) void linear_tile_kernel(LinArgs a) {
   using TIn = typename C::T;
   constexpr int FM = C::FM, FN = C::FN, SUB = C::SUB, NST = C::NST;
   constexpr int LPT = C::LA + C::LB;
@@ -428,10 +451,10 @@ __global__ __launch_bounds__(kThreads, C::OCC) void linear_tile_kernel(LinArgs a
   const TIn* A = (const TIn*)P.A;
   const TIn* B = (const TIn*)P.B;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = wave >> 1, wn = wave & 1;
+  const int wm = wave / C::WN, wn = wave % C::WN;
 
-  Operand<TIn, C::akm, C::BM, C::KSB, C::LA> oa;
-  Operand<TIn, C::bkm, C::BN, C::KSB, C::LB> ob;
+  Operand<TIn, C::akm, C::BM, C::WM, C::WAVES, C::KSB, C::LA> oa;
+  Operand<TIn, C::bkm, C::BN, C::WN, C::WAVES, C::KSB, C::LB> ob;
   oa.init(A, P.lda, m0, P.M, wm);
   ob.init(B, P.ldb, n0, P.N, wn);
 
@@ -508,7 +531,7 @@ __global__ __launch_bounds__(kThreads, C::OCC) void linear_tile_kernel(LinArgs a
   // summed by the workgroup whose tile column is g modulo the number of tile
   // columns, so every slice is summed once per tile row and the work is spread
   // evenly. A thread adds one 16-byte chunk of every RS-th k row of the slice.
-  constexpr int ACH = C::BM * C::ES / 16, RS = kThreads / ACH, EPC = C::EPC;
+  constexpr int ACH = C::BM * C::ES / 16, RS = C::THREADS / ACH, EPC = C::EPC;
   constexpr bool SUMS = KIND == EPI_PLAIN;
   float csum[SUMS ? EPC : 1];
   if constexpr (SUMS)
@@ -570,7 +593,66 @@ __global__ __launch_bounds__(kThreads, C::OCC) void linear_tile_kernel(LinArgs a
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  if (nk > 0) {
+  if constexpr (C::WAVES == 8) {
+    // Two wavefronts per SIMD take turns: while one multiplies a 16-deep step (bf16;
+    // 8 deep in fp32), the other reads its fragments for its next step and issues
+    // loads. The second group runs one barrier behind the first; every barrier ends
+    // one group's reads and the other's products. Slice k + 1 is loaded during the
+    // first two steps of slice k into the stage that both groups left a step ago.
+    if (nk > 0) {
+      issue(st0, 0);
+      wait_slice<0>();
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      const int group = __builtin_amdgcn_readfirstlane(wave >> 2);
+      if (group) __builtin_amdgcn_s_barrier();
+      auto turn = [&](unsigned char* cur, unsigned char* nxt, int k) __attribute__((always_inline)) {
+#pragma unroll
+        for (int s = 0; s < SUB; ++s) {
+          if constexpr (SUMS) {
+            if (s == 0 && k == next_sum) {
+              add_columns(cur);
+              next_sum += a.tiles_n;
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          read(cur, s, fa[0], fb[0]);
+          if (s < 2 && k + 1 < nk) {
+            const int64_t k0 = (int64_t)(s0 + k + 1) * C::KS;
+            if (s == 0)
+              oa.issue(nxt, k0, P.lda);
+            else
+              ob.issue(nxt + C::AB, k0, P.ldb);
+          }
+          // fragments are in; at the last step, so is this wavefront's part of
+          // slice k + 1
+          if (s == SUB - 1)
+            wait_slice<0>();
+          else
+            wait_lds();
+          __builtin_amdgcn_sched_barrier(0);
+          asm volatile("" ::: "memory");
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+          __builtin_amdgcn_s_setprio(1);
+          mma(fa[0], fb[0]);
+          __builtin_amdgcn_sched_barrier(0);
+          __builtin_amdgcn_s_setprio(0);
+          asm volatile("" ::: "memory");
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+        }
+      };
+      int k = 0;
+      for (; k + 2 <= nk; k += 2) {
+        turn(st0, st1, k);
+        turn(st1, st0, k + 1);
+      }
+      if (k < nk) turn(st0, st1, k);
+      if (!group) __builtin_amdgcn_s_barrier();
+    }
+  } else if (nk > 0) {
     issue(st0, 0);
     if (nk > 1) issue(st1, 1);
     if (NST > 2 && nk > 2) issue(st2, 2);
@@ -659,8 +741,8 @@ __global__ __launch_bounds__(kThreads, C::OCC) void linear_tile_kernel(LinArgs a
 #pragma unroll
     for (int j = 0; j < FN; ++j) asm volatile("" : "+a"(acc[i][j]));
 
-  float* reg = (float*)((wave < 2 ? st0 : st1) + (wave & 1) * C::PIECE);
-  const int row0 = m0 + wm * (C::BM / 2), col0 = n0 + wn * (C::BN / 2);
+  float* reg = (float*)((wave < C::WAVES / 2 ? st0 : st1) + (wave % (C::WAVES / 2)) * C::PIECE);
+  const int row0 = m0 + wm * (C::BM / C::WM), col0 = n0 + wn * (C::BN / C::WN);
   if (a.split > 1) {  // fp32 partial result, row-major like the result itself
     LinProblem q;
     q.M = P.M;
@@ -669,7 +751,7 @@ __global__ __launch_bounds__(kThreads, C::OCC) void linear_tile_kernel(LinArgs a
     q.e.ldd = a.ldpart;
     q.e.d_dtype = MAO_F32;
     q.e.add = nullptr;
-    finish_all<EPI_PLAIN, MAO_ACT_NONE, false, C::JU>(acc, reg, q, nullptr, row0, col0);
+    finish_all<EPI_PARTIAL, MAO_ACT_NONE, false, C::JU>(acc, reg, q, nullptr, row0, col0);
     return;
   }
   float* bias = (float*)(st1 + C::STAGE - C::BN * 4);
@@ -677,12 +759,12 @@ __global__ __launch_bounds__(kThreads, C::OCC) void linear_tile_kernel(LinArgs a
     if (threadIdx.x < C::BN) bias[threadIdx.x] = bias_v;
     __syncthreads();
   }
-  finish_any<KIND, BF, C::JU>(acc, reg, P, bias + wn * (C::BN / 2), row0, col0);
+  finish_any<KIND, BF, C::JU>(acc, reg, P, bias + wn * (C::BN / C::WN), row0, col0);
 }
 
 template <typename C, EpiKind KIND, bool BF>
 mao_status go(const LinArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((linear_tile_kernel<C, KIND, BF>), dim3(a.tiles * a.split), dim3(kThreads), 0, s,
+  hipLaunchKernelGGL((linear_tile_kernel<C, KIND, BF>), dim3(a.tiles * a.split), dim3(C::THREADS), 0, s,
                      a);
   MAO_LAUNCH_CHECK();
   return MAO_OK;
@@ -690,12 +772,16 @@ mao_status go(const LinArgs& a, hipStream_t s) {
 
 template <bool AKM, bool BKM, EpiKind KIND>
 mao_status pick(int dtype, int cfg, bool bf, const LinArgs& a, hipStream_t s) {
-  if (dtype == MAO_F32) return go<Cfg<float, AKM, BKM, 128, 128, 128, 2, 2>, KIND, false>(a, s);
+  if (dtype == MAO_F32) return go<Cfg<float, AKM, BKM, 128, 128, 2, 2, 128, 2, 2>, KIND, false>(a, s);
   constexpr bool BF = KIND != EPI_PLAIN;  // the weight gradient looks at its type
-  if (cfg == CFG_128x192) return go<Cfg<bf16_t, AKM, BKM, 128, 192, 128, 2, 2>, KIND, BF>(a, s);
-  if (cfg == CFG_192x128) return go<Cfg<bf16_t, AKM, BKM, 192, 128, 128, 2, 2>, KIND, BF>(a, s);
-  if (BF && bf) return go<Cfg<bf16_t, AKM, BKM, 128, 128, 128, 2, 2>, KIND, BF>(a, s);
-  return go<Cfg<bf16_t, AKM, BKM, 128, 128, 128, 2, 2>, KIND, false>(a, s);
+  switch (cfg) {
+    case CFG_256x256: return go<Cfg<bf16_t, AKM, BKM, 256, 256, 4, 2, 128, 2, 2>, KIND, BF>(a, s);
+    case CFG_256x192: return go<Cfg<bf16_t, AKM, BKM, 256, 192, 4, 2, 128, 2, 2>, KIND, BF>(a, s);
+    case CFG_128x192: return go<Cfg<bf16_t, AKM, BKM, 128, 192, 2, 2, 128, 2, 2>, KIND, BF>(a, s);
+    case CFG_192x128: return go<Cfg<bf16_t, AKM, BKM, 192, 128, 2, 2, 128, 2, 2>, KIND, BF>(a, s);
+  }
+  if (BF && bf) return go<Cfg<bf16_t, AKM, BKM, 128, 128, 2, 2, 128, 2, 2>, KIND, BF>(a, s);
+  return go<Cfg<bf16_t, AKM, BKM, 128, 128, 2, 2, 128, 2, 2>, KIND, false>(a, s);
 }
 
 }  // namespace

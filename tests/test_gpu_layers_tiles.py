@@ -1,0 +1,113 @@
+"""The linear layer's products on every tile shape and with K split (GPU).
+
+Ragged sizes for which the cut by estimated time comes out as each tile shape, alone
+or with K split over workgroups; each product against float64 (torch, on the GPU)
+with the bounds of test_gpu_layers: (K + 8) 2^-24 of the magnitudes multiplied, then
+one rounding of the result.
+"""
+import math
+
+import pytest
+
+from tests.helpers import log
+from tests.test_gpu_layers import B, U
+
+pytestmark = pytest.mark.gpu
+
+
+def _rows(t):
+    import torch
+    r, c = t.shape
+    buf = torch.full((r, (c + 7) // 8 * 8), math.nan, dtype=t.dtype, device="cuda")
+    buf[:, :c] = t
+    return buf[:, :c]
+
+
+def _normal(g, r, c, scale=1.0):
+    import torch
+    x = torch.randn((r, c), generator=g, device="cuda") * scale
+    return _rows(x.bfloat16())
+
+
+def _gen(seed):
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _check(got, want, bound, what):
+    err = (got.double() - want).abs()
+    assert bool((err <= bound).all()), (what, float((err / bound).max()))
+
+
+def _gelu_tanh(z):
+    import torch
+    s = torch.sigmoid(2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3))
+    ds = s * (1 - s) * 2 * math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * z * z)
+    return z * s, s + z * ds
+
+
+# 128x128, 128x128 split, 128x192, split, 192x128, split, 256x192, 256x256, split
+FWD = [(123, 77, 88), (104, 790, 68), (674, 344, 5453), (5621, 3205, 141), (938, 327, 4325),
+       (140, 3469, 5612), (3896, 79, 2079), (6184, 71, 2000), (5008, 5977, 1179)]
+
+
+@pytest.mark.parametrize("rows,k,n", FWD)
+def test_forward_tiles(gpu_lib, rows, k, n):
+    import torch
+    log(f"forward tiles {rows} {k} {n}")
+    g = _gen(rows)
+    x, w = _normal(g, rows, k), _normal(g, n, k, 1 / math.sqrt(k))
+    bias, res = torch.randn(n, generator=g, device="cuda"), _normal(g, rows, n)
+    z = _normal(g, rows, n)
+    y = gpu_lib.linear(x, w, bias, act="gelu_tanh", residual=res, preact=z)
+    xd, wt = x.double(), w.double().t().contiguous()
+    wz = torch.matmul(xd, wt) + bias.double()
+    bz = (k + 8) * U * torch.matmul(xd.abs(), wt.abs()) + 2 * U * (wz.abs() + bias.abs())
+    _check(z, wz, bz + B * (wz.abs() + bz), "z")
+    wy = _gelu_tanh(wz)[0] + res.double()
+    by = 1.2 * bz + 2e-6 * wz.abs().clamp(min=1) + U * (wy.abs() + res.double().abs())
+    _check(y, wy, by + B * (wy.abs() + by), "y")
+
+
+DX = [(123, 77, 88), (142, 82, 883), (2219, 1994, 325), (910, 1305, 4768), (4987, 837, 324),
+      (146, 5530, 3508), (6137, 1296, 71), (5567, 2188, 70), (4907, 1154, 5826)]
+
+
+@pytest.mark.parametrize("rows,k,n", DX)
+def test_input_gradient_tiles(gpu_lib, rows, k, n):
+    import torch
+    log(f"input gradient tiles {rows} {k} {n}")
+    g = _gen(rows + 1)
+    dy, w = _normal(g, rows, n), _normal(g, n, k, 1 / math.sqrt(n))
+    add, z = _normal(g, rows, k), _normal(g, rows, k, 2.0)
+    z8 = gpu_lib.q8_quantize(z, "int8")
+    dx = gpu_lib.linear_backward_input(dy, w, act="gelu_tanh", preact=z8, add=add)
+    zv = z8.codes.double() * torch.exp2(z8.scales.double() - 127).repeat_interleave(32, 1)[:, :k]
+    dd, wd = dy.double(), w.double().contiguous()
+    p = torch.matmul(dd, wd)
+    want = p * _gelu_tanh(zv)[1] + add.double()
+    bound = 1.2 * (n + 8) * U * torch.matmul(dd.abs(), wd.abs()) + U * (want.abs() + add.double().abs())
+    bound = bound + 2e-6 * zv.abs().clamp(min=1) * p.abs()
+    _check(dx, want, bound + B * (want.abs() + bound), "dx")
+
+
+DW = [(123, 77, 88), (1254, 90, 67), (338, 4623, 780), (4485, 1324, 908), (336, 775, 4922),
+      (7193, 3460, 133), (67, 2321, 5181), (6640, 1160, 4962)]
+
+
+@pytest.mark.parametrize("rows,k,n", DW)
+def test_weight_gradient_tiles(gpu_lib, rows, k, n):
+    import torch
+    log(f"weight gradient tiles {rows} {k} {n}")
+    g = _gen(rows + 2)
+    dy, x = _normal(g, rows, n), _normal(g, rows, k)
+    for out in (torch.float32, torch.bfloat16):
+        dw, db = gpu_lib.linear_backward_weight(dy, x, dtype=out)
+        dt, xd = dy.double().t().contiguous(), x.double().contiguous()
+        want = torch.matmul(dt, xd)
+        bound = (rows + 8) * U * torch.matmul(dt.abs(), xd.abs())
+        r = B if out == torch.bfloat16 else U
+        _check(dw, want, bound + r * (want.abs() + bound), "dw")
+        _check(db, dt.sum(1), (rows + 8) * U * dt.abs().sum(1), "dbias")
