@@ -70,15 +70,21 @@ __device__ __forceinline__ void group_total2(float& a, float& b, float2* buf) {
   a = wave_total(a);
   b = wave_total(b);
   if constexpr (TPR > 64) {
-    const int w = threadIdx.x >> 6, w0 = w / (TPR / 64) * (TPR / 64);
+    constexpr int NW = TPR / 64;
+    const int w = threadIdx.x >> 6, w0 = w / NW * NW;
     if ((threadIdx.x & 63) == 0) buf[w] = make_float2(a, b);
     __syncthreads();
-    a = b = 0.f;
-#pragma unroll
-    for (int i = 0; i < TPR / 64; ++i) {
-      const float2 t = buf[w0 + i];
-      a += t.x;
-      b += t.y;
+    if constexpr (NW == 3) {
+      const float2 t0 = buf[w0], t1 = buf[w0 + 1], t2 = buf[w0 + 2];
+      a = (t0.x + t1.x) + t2.x;
+      b = (t0.y + t1.y) + t2.y;
+    } else {  // one partial sum per lane, joined across 2, 4, 8 or 16 lanes
+      const float2 t = buf[w0 + (threadIdx.x & (NW - 1))];
+      a = dpp_add<0xB1>(t.x);
+      b = dpp_add<0xB1>(t.y);
+      if constexpr (NW >= 4) a = dpp_add<0x4E>(a), b = dpp_add<0x4E>(b);
+      if constexpr (NW >= 8) a = dpp_add<0x141>(a), b = dpp_add<0x141>(b);
+      if constexpr (NW >= 16) a = dpp_add<0x140>(a), b = dpp_add<0x140>(b);
     }
   }
 }
@@ -254,8 +260,11 @@ __global__ __launch_bounds__(BLK) void norm_bwd_kernel(NormBwdArgs a) {
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int i = 0; i < 8; ++i) dg[v][i] = db[v][i] = 0.f;
+  // the joining gradient comes with its row where it has dY's type (the usual
+  // case), otherwise as it is needed
+  const bool add_early = a.add != nullptr && a.add_dtype == (sizeof(TDy) == 2 ? MAO_BF16 : MAO_F32);
   struct Row {
-    Raw8<TDy> dy[V];
+    Raw8<TDy> dy[V], add[V];
     SavedRaw<XK> x[V];
     float mean, rstd;
   };
@@ -269,6 +278,7 @@ __global__ __launch_bounds__(BLK) void norm_bwd_kernel(NormBwdArgs a) {
       if (c < nch) {
         q.dy[v].load((const TDy*)a.dy + row * a.lddy + 8 * c);
         q.x[v].load(a, row, c);
+        if (add_early) q.add[v].load((const TDy*)a.add + row * a.ldadd + 8 * c);
       } else {
         q.dy[v].zero();
         q.x[v].zero();
@@ -325,7 +335,10 @@ __global__ __launch_bounds__(BLK) void norm_bwd_kernel(NormBwdArgs a) {
       for (int i = 0; i < 8; ++i) o[i] = q.rstd * (g[i] - c0 - xh[i] * c1);
       if (a.add) {
         float w[8];
-        load8_any(a.add, a.add_dtype, (int64_t)row * a.ldadd + 8 * c, w);
+        if (add_early)
+          q.add[v].get(w);
+        else
+          load8_any(a.add, a.add_dtype, (int64_t)row * a.ldadd + 8 * c, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] += w[i];
       }
@@ -341,7 +354,8 @@ __global__ __launch_bounds__(BLK) void norm_bwd_kernel(NormBwdArgs a) {
       handle(q, r0 + sub, red[k]);
     }
   } else {
-    // two rows in turn: the next one is on its way while one is handled
+    // two rows in turn: the next one is on its way while one is handled (a third
+    // row in flight gained nothing)
     Row q0, q1;
     fetch(q0, (int64_t)r0 + sub);
     while (true) {
@@ -393,7 +407,7 @@ __global__ __launch_bounds__(BLK) void norm_bwd_kernel(NormBwdArgs a) {
 
 // Threads per workgroup; the backward pass takes more, for fewer partial rows.
 constexpr int fwd_block(int tpr) { return tpr > 256 ? tpr : 256; }
-constexpr int bwd_block(int tpr) { return tpr > 64 ? 1024 : 512; }
+constexpr int bwd_block(int tpr) { return 1024 / tpr * tpr; }
 
 template <typename TIn, int TPR, int V>
 mao_status fwd_launch(const NormFwdArgs& a, hipStream_t s) {
@@ -421,11 +435,12 @@ struct BwdShape {
   int tpr, v;
 };
 BwdShape bwd_shape(int64_t cols) {
-  // A wavefront holds up to three runs per lane beside the column sums, two rows
-  // in flight and gamma; wider rows take one run per thread of a 1024-thread
-  // workgroup, which keeps 16 wavefronts on the CU (4093 x 4096 from 8 bits: two
-  // runs per thread and 8 wavefronts 26.7 us).
-  if (cols <= 1536) return {64, (int)ceil_div(cols, 512)};
+  // One run per thread: column sums, gamma and two or three rows in flight fit
+  // 128 registers, so that 16 wavefronts share a CU. (16384 x 1536 bf16: three runs
+  // per lane of one wavefront, 8 wavefronts per CU, 50.8 us.)
+  if (cols <= 512) return {64, 1};
+  if (cols <= 1024) return {128, 1};
+  if (cols <= 1536) return {192, 1};
   if (cols <= 2048) return {256, 1};
   if (cols <= 4096) return {512, 1};
   return {1024, cols <= 8192 ? 1 : cols <= 16384 ? 2 : 4};
@@ -444,10 +459,9 @@ template <typename TDy, int XK>
 mao_status bwd_pick(const NormBwdArgs& a, hipStream_t s) {
   const BwdShape b = bwd_shape(a.cols);
   switch (b.tpr) {
-    case 64:
-      if (b.v == 1) return bwd_launch<TDy, XK, 64, 1>(a, s);
-      if (b.v == 2) return bwd_launch<TDy, XK, 64, 2>(a, s);
-      return bwd_launch<TDy, XK, 64, 3>(a, s);
+    case 64: return bwd_launch<TDy, XK, 64, 1>(a, s);
+    case 128: return bwd_launch<TDy, XK, 128, 1>(a, s);
+    case 192: return bwd_launch<TDy, XK, 192, 1>(a, s);
     case 256: return bwd_launch<TDy, XK, 256, 1>(a, s);
     case 512: return bwd_launch<TDy, XK, 512, 1>(a, s);
     default:

@@ -165,8 +165,7 @@ struct LinProblem {
   int a_km, b_km;
   LinEpilogue e;
 };
-// km: both operands K-major (the weight gradient).
-size_t lin_workspace(int dtype, bool km, int64_t M, int64_t N, int64_t K);
+size_t lin_workspace(int dtype, int64_t M, int64_t N, int64_t K);
 // sums (weight gradient, or nullptr): lin_sum_rows x M floats that receive
 // partial column sums of A.
 int lin_sum_rows(int dtype, int64_t M, int64_t N, int64_t K);

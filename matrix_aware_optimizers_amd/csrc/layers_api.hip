@@ -103,7 +103,7 @@ WeightWs carve_weight(void* base, int64_t rows, int64_t k, int64_t n, int dtype,
   WeightWs w = {};
   w.ldx = ws_ld(k);
   if (rebuilt) w.x = c.take<char>((size_t)rows * w.ldx * dtype_size(dtype));
-  w.part = c.take<char>(lin_workspace(dtype, true, n, k, rows));
+  w.part = c.take<char>(lin_workspace(dtype, n, k, rows));
   w.sums = c.take<float>((size_t)lin_sum_rows(dtype, n, k, rows) * n);
   w.bytes = c.used;
   return w;
@@ -251,13 +251,13 @@ mao_status mao_layer_norm_backward(mao_mat dY, const mao_mat* X, const mao_q8* X
 
 size_t mao_linear_workspace_size(int64_t rows, int64_t k, int64_t n, int32_t dtype) {
   if (!sizes_ok(rows, k, n) || !dtype_ok(dtype) || rows <= kTokenRows) return 0;
-  return lin_workspace(dtype, false, rows, n, k);
+  return lin_workspace(dtype, rows, n, k);
 }
 
 size_t mao_linear_backward_input_workspace_size(int64_t rows, int64_t k, int64_t n,
                                                 int32_t dtype) {
   if (!sizes_ok(rows, k, n) || !dtype_ok(dtype)) return 0;
-  return lin_workspace(dtype, false, rows, k, n);
+  return lin_workspace(dtype, rows, k, n);
 }
 
 size_t mao_linear_backward_weight_workspace_size(int64_t rows, int64_t k, int64_t n, int32_t dtype,

@@ -322,7 +322,8 @@ __device__ __forceinline__ int swz_k(int row) {
 template <int BX, int ES>
 __device__ __forceinline__ int swz_m(int krow) {
   if (ES == 4) return ((krow >> 2) & 1) << 3;
-  return BX == 192 ? ((krow >> 1) & 1) << 2 : (krow & 3) << 2;
+  // rows of 384 or 128 bytes already alternate between the halves of the banks
+  return BX == 192 || BX == 64 ? ((krow >> 1) & 1) << 2 : (krow & 3) << 2;
 }
 
 // Per-thread global sources of one operand's direct loads, and its LDS fragment
@@ -772,7 +773,10 @@ mao_status go(const LinArgs& a, hipStream_t s) {
 
 template <bool AKM, bool BKM, EpiKind KIND>
 mao_status pick(int dtype, int cfg, bool bf, const LinArgs& a, hipStream_t s) {
-  if (dtype == MAO_F32) return go<Cfg<float, AKM, BKM, 128, 128, 2, 2, 128, 2, 2>, KIND, false>(a, s);
+  if (dtype == MAO_F32) {
+    if (cfg == CFG_64x64) return go<Cfg<float, AKM, BKM, 64, 64, 2, 2, 128, 2, 4>, KIND, false>(a, s);
+    return go<Cfg<float, AKM, BKM, 128, 128, 2, 2, 128, 2, 2>, KIND, false>(a, s);
+  }
   constexpr bool BF = KIND != EPI_PLAIN;  // the weight gradient looks at its type
   switch (cfg) {
     case CFG_256x256: return go<Cfg<bf16_t, AKM, BKM, 256, 256, 4, 2, 128, 2, 2>, KIND, BF>(a, s);
@@ -780,6 +784,7 @@ mao_status pick(int dtype, int cfg, bool bf, const LinArgs& a, hipStream_t s) {
     case CFG_128x192: return go<Cfg<bf16_t, AKM, BKM, 128, 192, 2, 2, 128, 2, 2>, KIND, BF>(a, s);
     case CFG_192x128: return go<Cfg<bf16_t, AKM, BKM, 192, 128, 2, 2, 128, 2, 2>, KIND, BF>(a, s);
   }
+  if (cfg == CFG_64x64) return go<Cfg<bf16_t, AKM, BKM, 64, 64, 2, 2, 128, 2, 4>, KIND, false>(a, s);
   if (BF && bf) return go<Cfg<bf16_t, AKM, BKM, 128, 128, 2, 2, 128, 2, 2>, KIND, BF>(a, s);
   return go<Cfg<bf16_t, AKM, BKM, 128, 128, 2, 2, 128, 2, 2>, KIND, false>(a, s);
 }
