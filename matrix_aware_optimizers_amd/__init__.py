@@ -462,11 +462,7 @@ class Q8:
 
     def __init__(self, codes, scales):
         torch = _torch()
-        if codes.dtype == torch.int8:
-            fmt = 0
-        elif codes.dtype == torch.float8_e4m3fn:
-            fmt = 1
-        else:
+        if codes.dtype not in (torch.int8, torch.float8_e4m3fn):
             raise TypeError(f"codes must be int8 or float8_e4m3fn, not {codes.dtype}")
         if scales.dtype != torch.uint8:
             raise TypeError("scales must be uint8")
@@ -478,12 +474,13 @@ class Q8:
         if scales.device != codes.device:
             raise ValueError("codes and scales must share a device")
         self.codes, self.scales = codes, scales
-        self.c = Q8C(codes.data_ptr(), scales.data_ptr(), codes.shape[0], codes.shape[1],
-                     codes.stride(0), scales.stride(0), fmt)
 
     shape = property(lambda self: self.codes.shape)
     device = property(lambda self: self.codes.device)
-    fmt = property(lambda self: "e4m3" if self.c.format else "int8")
+    fmt = property(lambda self: "int8" if self.codes.dtype == _torch().int8 else "e4m3")
+
+    def get_device(self):
+        return self.codes.get_device()
 
 
 def q8_empty(rows, cols, fmt="int8", device=None) -> Q8:
@@ -495,255 +492,117 @@ def q8_empty(rows, cols, fmt="int8", device=None) -> Q8:
     return Q8(codes[:, :cols], torch.empty((rows, blocks), dtype=torch.uint8, device=device))
 
 
-# These calls are made per layer and, decoding, per token: the binding keeps to
-# one look at each tensor and caches what depends on sizes alone.
+# The marshalling itself is in csrc/binding.cpp (``_layers.so``): these calls are made
+# per layer and, decoding, per token. Here are names, defaults, streams and workspaces.
 
+_layers = None
 _layer_ws: dict = {}
-_codes: dict = {}
 
 
-def _setup():
+def _load_layers():
+    """Loads _layers.so (raises if it has not been built)."""
+    global _layers, _get_device, _get_stream
+    load()
     torch = _torch()
-    _codes[torch.float32] = F32
-    _codes[torch.bfloat16] = BF16
+    path = os.path.join(_HERE, "_layers.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} not found: build it with `python -m matrix_aware_optimizers_amd.build`")
+    import importlib.util
+    spec = importlib.util.spec_from_file_location("_layers", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.init(_layer_workspace, _check, Q8)
     # the current device and stream as numbers, without building objects
-    global _get_device, _get_stream
     _get_device = torch._C._cuda_getDevice
     _get_stream = torch._C._cuda_getCurrentRawStream
+    _layers = mod
 
 
-def _mat(t) -> Mat:
-    """mat() for the calls below: one row may have any row stride."""
-    try:
-        rows, cols = t.shape
-        ld, unit = t.stride()
-    except ValueError:
-        raise ValueError("expected a 2-D row-major tensor (unit column stride)") from None
-    if unit != 1 and cols != 1:
-        raise ValueError("expected a 2-D row-major tensor (unit column stride)")
-    if rows == 1:
-        ld = (cols + 7) & ~7
-    code = _codes.get(t.dtype)
-    if code is None:
-        raise TypeError(f"unsupported dtype {t.dtype}")
-    return Mat(t.data_ptr(), rows, cols, ld, code)
-
-
-def _matp(t):
-    return None if t is None else ctypes.byref(_mat(t))
-
-
-def _new(rows, cols, dtype, device):
-    if cols % 8:
-        return empty_matrix(rows, cols, dtype, device)
-    return _torch().empty((rows, cols), dtype=dtype, device=device)
-
-
-def _vec(t, n, name):
-    """(address, dtype code) of an optional contiguous vector of n values."""
-    if t is None:
-        return None, F32
-    if t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous vector of {n} values")
-    code = _codes.get(t.dtype)
-    if code is None:
-        raise TypeError(f"unsupported dtype {t.dtype} of {name}")
-    return t.data_ptr(), code
-
-
-def _floats(t, n, name):
-    p, code = _vec(t, n, name)
-    if code != F32:
-        raise TypeError(f"{name} must be float32")
-    return p
-
-
-def _act_code(act):
-    return ACTS[act] if isinstance(act, str) else int(act)
-
-
-def _split(x):
-    """(matrix pointer, checkpoint pointer) of a tensor, a Q8 or None."""
-    if isinstance(x, Q8):
-        return None, ctypes.byref(x.c)
-    return _matp(x), None
-
-
-def _device(first, *rest):
-    """The device all tensors are on (entry points take one device's tensors)."""
-    if not _codes:
-        _setup()
-    dev = first.device
-    if dev.type != "cuda":
-        raise ValueError(f"tensors must be on the GPU, not on {dev}")
-    for t in rest:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
-    return dev
-
-
-def _workspace(nbytes, dev, stream):
-    """(address, bytes) of a buffer that only this stream's calls share, and the
-    object that keeps it. Under graph capture it is the graph's own, so that a
-    later, larger call cannot take it away from the graph."""
-    if nbytes == 0:
-        return None, 0, None
+def _layer_workspace(nbytes, index, stream):
+    """A byte tensor that only this stream's calls share. Under graph capture it is
+    the graph's own, so that a later, larger call cannot take it away from the
+    graph."""
     torch = _torch()
     if torch.cuda.is_current_stream_capturing():
-        buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        return buf.data_ptr(), nbytes, buf
-    key = (dev.index, stream)
+        return torch.empty(nbytes, dtype=torch.uint8, device=index)
+    key = (index, stream)
     buf = _layer_ws.get(key)
     if buf is None or buf.numel() < nbytes:
-        buf = _layer_ws[key] = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    return buf.data_ptr(), buf.numel(), buf
+        buf = _layer_ws[key] = torch.empty(nbytes, dtype=torch.uint8, device=index)
+    return buf
 
 
-_sizes: dict = {}
+def _run(fn, first, *args):
+    """fn(first, *args, device, stream) of the binding on the current stream of
+    first's device."""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("tensors must be on the GPU")
+    if _layers is None:
+        _load_layers()
+    if _get_device() == index:
+        return getattr(_layers, fn)(first, *args, index, _get_stream(index))
+    with _torch().cuda.device(index):
+        return getattr(_layers, fn)(first, *args, index, _get_stream(index))
 
 
-def _ws_bytes(name, *args):
-    key = (name, args)
-    n = _sizes.get(key)
-    if n is None:
-        n = _sizes[key] = getattr(load(), name)(*args)
-        if len(_sizes) > 4096:  # lengths that keep changing
-            _sizes.clear()
-    return n
-
-
-def _call(name, dev, args, nbytes=None):
-    """Runs an entry point on dev's current stream; with ``nbytes``, a workspace
-    of that size goes in front of the stream."""
-    if _get_device() != dev.index:
-        with _torch().cuda.device(dev):
-            return _call(name, dev, args, nbytes)
-    stream = _get_stream(dev.index)
-    fn = getattr(_lib or load(), name)
-    if nbytes is None:
-        status = fn(*args, stream)
-    else:
-        ws, have, keep = _workspace(nbytes, dev, stream)
-        status = fn(*args, ws, have, stream)
-        del keep
-    if status:
-        _check(status, name)
+def _act(act):
+    if isinstance(act, str):
+        if act not in ACTS:
+            raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACTS)}")
+        return ACTS[act]
+    return int(act)
 
 
 def q8_quantize(X, fmt="int8", out=None) -> Q8:
     """Keeps X (bf16 or fp32) in 8 bits."""
-    dev = _device(X, out)
     if out is None:
-        out = q8_empty(X.shape[0], X.shape[1], fmt, dev)
-    _call("mao_q8_quantize", dev, (_mat(X), ctypes.byref(out.c)))
+        out = q8_empty(X.shape[0], X.shape[1], fmt, X.device)
+    _run("q8_quantize", X, out.codes, out.scales)
     return out
 
 
 def q8_dequantize(q: Q8, act="none", dtype=None, out=None):
     """act(q) as a tensor (bf16 unless ``dtype`` or ``out`` says fp32)."""
-    dev = _device(q, out)
-    if out is None:
-        out = _new(q.shape[0], q.shape[1], dtype or _torch().bfloat16, dev)
-    _call("mao_q8_dequantize", dev, (ctypes.byref(q.c), _act_code(act), _mat(out)))
-    return out
+    return _run("q8_dequantize", q, _act(act),
+                F32 if dtype is not None and dtype == _torch().float32 else BF16, out)
 
 
 def layer_norm(X, gamma=None, beta=None, *, eps=1e-5, out=None, stats=True):
     """(Y, mean, rstd) of layer norm over the rows of X; the statistics are None
     without ``stats``."""
-    dev = _device(X, gamma, beta, out)
-    x = _mat(X)
-    rows, cols = x.rows, x.cols
-    if out is None:
-        out = _new(rows, cols, X.dtype, dev)
-    mean = rstd = None
-    if stats:
-        torch = _torch()
-        mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=dev).unbind(0)
-    g, gd = _vec(gamma, cols, "gamma")
-    b, bd = _vec(beta, cols, "beta")
-    if g is not None and b is not None and gd != bd:
-        raise TypeError("gamma and beta must share a dtype")
-    _call("mao_layer_norm", dev,
-          (x, g, b, gd if g is not None else bd, eps, _mat(out),
-           mean.data_ptr() if stats else None, rstd.data_ptr() if stats else None))
-    return out, mean, rstd
+    return _run("layer_norm", X, gamma, beta, eps, out, bool(stats))
 
 
 def layer_norm_backward(dY, X, gamma, mean, rstd, *, add=None, out=None, dgamma=None, dbeta=None):
     """(dX, dgamma, dbeta) of layer_norm. X: its input, or the input's Q8
     checkpoint. ``add`` joins dX (the skip connection's gradient)."""
-    dev = _device(dY, X, gamma, mean, rstd, add, out, dgamma, dbeta)
-    dy = _mat(dY)
-    rows, cols = dy.rows, dy.cols
-    if mean is None or rstd is None:
-        raise ValueError("mean and rstd of the forward pass are needed")
-    if out is None:
-        out = _new(rows, cols, dY.dtype, dev)
-    torch = _torch()
-    if dgamma is None:
-        dgamma = torch.empty(cols, dtype=torch.float32, device=dev)
-    if dbeta is None:
-        dbeta = torch.empty(cols, dtype=torch.float32, device=dev)
-    g, gd = _vec(gamma, cols, "gamma")
-    x, x8 = _split(X)
-    _call("mao_layer_norm_backward", dev,
-          (dy, x, x8, g, gd, _floats(mean, rows, "mean"), _floats(rstd, rows, "rstd"), _matp(add),
-           _mat(out), _floats(dgamma, cols, "dgamma"), _floats(dbeta, cols, "dbeta")),
-          _ws_bytes("mao_layer_norm_backward_workspace_size", rows, cols))
-    return out, dgamma, dbeta
+    return _run("layer_norm_backward", dY, X, gamma, mean, rstd, add, out, dgamma, dbeta)
 
 
 def linear(X, W, bias=None, *, act="none", residual=None, out=None, preact=None):
     """act(X W^T + bias) + residual. ``preact``: a tensor that receives the value
     before the activation; ``out`` may be ``residual``."""
-    dev = _device(X, W, bias, residual, out, preact)
-    x, w = _mat(X), _mat(W)
-    if out is None:
-        out = _new(x.rows, w.rows, X.dtype, dev)
-    b, bd = _vec(bias, w.rows, "bias")
-    _call("mao_linear", dev,
-          (x, w, b, bd, _act_code(act), _matp(residual), _mat(out), _matp(preact)),
-          _ws_bytes("mao_linear_workspace_size", x.rows, x.cols, w.rows, x.dtype))
-    return out
+    return _run("linear", X, W, bias, _act(act), residual, out, preact)
 
 
 def linear_backward_input(dY, W, *, act="none", preact=None, add=None, out=None):
     """(dY W) * act'(preact) + add: the gradient of the layer's input, taken back
     through the activation that made it. ``preact``: a tensor or a Q8."""
-    dev = _device(dY, W, preact, add, out)
-    dy, w = _mat(dY), _mat(W)
-    if out is None:
-        out = _new(dy.rows, w.cols, dY.dtype, dev)
-    z, z8 = _split(preact)
-    _call("mao_linear_backward_input", dev,
-          (dy, w, _act_code(act), z, z8, _matp(add), _mat(out)),
-          _ws_bytes("mao_linear_backward_input_workspace_size", dy.rows, w.cols, w.rows, dy.dtype))
-    return out
+    return _run("linear_backward_input", dY, W, _act(act), preact, add, out)
 
 
 def linear_backward_weight(dY, X, *, x_act="none", dtype=None, out=None, dbias=None,
                            accumulate=False):
-    """(dW, dbias) = (dY^T x_act(X), column sums of dY). X: the layer's input or
-    its Q8 checkpoint. With ``accumulate`` both are added to ``out`` and
-    ``dbias``, which then have to be given."""
-    dev = _device(dY, X, out, dbias)
+    """(dW, dbias) = (dY^T x_act(X), column sums of dY), dW in fp32 unless ``dtype``
+    or ``out`` says bf16. X: the layer's input or its Q8 checkpoint. With
+    ``accumulate`` both are added to ``out`` and ``dbias``, which then have to be
+    given."""
     if accumulate and (out is None or dbias is None):
         raise ValueError("accumulate needs out and dbias")
-    torch = _torch()
-    dy = _mat(dY)
-    rows, n, k = dy.rows, dy.cols, X.shape[1]
-    if out is None:
-        out = _new(n, k, dtype or torch.float32, dev)
-    if dbias is None:
-        dbias = torch.empty(n, dtype=torch.float32, device=dev)
-    code = _act_code(x_act)
-    x, x8 = _split(X)
-    _call("mao_linear_backward_weight", dev,
-          (dy, x, x8, code, _mat(out), _floats(dbias, n, "dbias"), 1 if accumulate else 0),
-          _ws_bytes("mao_linear_backward_weight_workspace_size", rows, k, n, dy.dtype,
-                    1 if x8 is not None or code else 0))
-    return out, dbias
+    return _run("linear_backward_weight", dY, X, _act(x_act),
+                BF16 if dtype is not None and dtype == _torch().bfloat16 else F32, out, dbias,
+                bool(accumulate))
 
 
 def _as_batch(X):

@@ -3,7 +3,8 @@
 Usage: ``python -m matrix_aware_optimizers_amd.build`` (or call ``build()``).
 Every ``.hip`` file under ``csrc/`` is compiled to an object with hipcc for
 gfx950 and the objects are linked into ``libmao.so``. Objects go to
-``_build/`` at the repository root.
+``_build/`` at the repository root. ``csrc/binding.cpp`` (host code: torch
+tensors to the C ABI, for the layer operators) becomes ``_layers.so`` beside it.
 """
 from __future__ import annotations
 
@@ -12,12 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmao.so")
+BINDING = os.path.join(HERE, "_layers.so")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -42,21 +45,50 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_binding() -> str:
+    """The object of csrc/binding.cpp (needs the headers of torch and Python)."""
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(OBJ, "binding.o")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c",
+          f"-I{inc}", f"-I{inc}/torch/csrc/api/include", f"-I{sysconfig.get_paths()['include']}",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          os.path.join(CSRC, "binding.cpp"), "-o", obj], "g++ on binding.cpp")
+    return obj
+
+
+def _link_binding(obj: str):
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    _run(["g++", "-shared", "-o", tmp, obj, LIB, f"-L{lib}", "-ltorch_python", "-ltorch_cpu",
+          "-lc10", "-Wl,-rpath,$ORIGIN"], "link of _layers.so")
+    shutil.move(tmp, BINDING)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source for gfx950 and link libmao.so; returns its path."""
+    """Compile every HIP source for gfx950 and link libmao.so (and _layers.so);
+    returns its path."""
     if not os.path.exists(HIPCC):
         raise RuntimeError(f"hipcc not found at {HIPCC}")
     os.makedirs(OBJ, exist_ok=True)
     srcs = sources()
     workers = min(len(srcs), max(1, (os.cpu_count() or 2) // 2))
     with cf.ThreadPoolExecutor(max_workers=workers) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, srcs))
+        binding = binding.result()
     tmp = LIB + ".tmp"
-    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Wl,-soname,libmao.so", "-o", tmp,
+          *objs], "link of libmao.so")
     shutil.move(tmp, LIB)
+    _link_binding(binding)
     if verbose:
         print(f"built {LIB}")
     return LIB

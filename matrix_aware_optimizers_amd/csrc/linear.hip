@@ -1,8 +1,6 @@
 // How the linear layer's products are cut into tiles and K splits.
 #include "linear.hpp"
 
-#include <math.h>
-
 #include <algorithm>
 
 namespace mao {
@@ -23,24 +21,28 @@ struct Shape {
   double rate, ends;
 };
 const Shape kShapes[CFG_COUNT] = {
-    {256, 256, 1, 5.1, 10.0}, {256, 192, 1, 5.0, 8.5},  {128, 192, 2, 5.0, 10.5},
-    {192, 128, 2, 5.0, 9.0},  {128, 128, 2, 4.25, 7.5}, {64, 64, 4, 2.7, 5.7},
+    {256, 256, 1, 5.43, 11.4}, {256, 192, 1, 4.95, 8.6}, {128, 192, 2, 5.2, 9.7},
+    {192, 128, 2, 5.2, 9.1},   {128, 128, 2, 4.2, 6.9},  {64, 64, 3, 2.5, 4.9},
 };
-constexpr double kF32Rate[2] = {0.485, 0.545};  // 128 x 128 and 64 x 64 tiles
+constexpr double kF32Rate[2] = {0.485, 0.53};  // 128 x 128 and 64 x 64 tiles
 
 // The cut with the shortest estimated time. Tiles run in rounds of 256 workgroups
 // times those that share a CU; a last round that is not full is shorter too (the
-// clock rises as CUs idle). Of p workgroups that fit a CU, o take (o / p)^0.6 of the
-// time of p. With few tiles K is split: more workgroups, then a launch and one pass
+// clock rises as CUs idle). Of p workgroups that fit a CU, o take the square root
+// of o / p of the time of p. With few tiles K is split: more workgroups, then a launch and one pass
 // over the partial results.
 //
-// The constants minimise the loss over 99 products (three layouts, both types, 77
-// to 16384 rows, K from 200 to 16384) timed with every shape and up to ten splits
-// on MI355X: the estimate's choice is 2.9% slower than the best one on average,
-// 14% at worst (6144 x 1536 x 16384 with one K-contiguous operand).
-Plan make_plan(int dtype, bool mixed, int64_t M, int64_t N, int64_t K) {
+// The constants minimise the loss over 117 products (three layouts, both types, 77
+// to 16384 rows, K from 200 to 16384, operands not in the L2) timed with every shape
+// and up to 14 splits on MI355X: the estimate's choice is 2% slower than the best
+// one on average, 15% at worst (512 x 4096 x 4096, 40 against 35 us).
+Plan estimate_plan(int dtype, bool mixed, int64_t M, int64_t N, int64_t K) {
+  // sqrt(o / p) for o = 1 .. p
+  static const double kShare[5][4] = {
+      {}, {1.0}, {0.707, 1.0}, {0.577, 0.816, 1.0}, {0.5, 0.707, 0.866, 1.0}};
   const int ks = dtype == MAO_BF16 ? 64 : 32;
-  const int64_t slices = ceil_div(K, ks);
+  const int slices = (int)ceil_div(K, ks);
+  const double part_us = 8.0 * M * N / 1e7;
   Plan best = {};
   double best_us = 0.0;
   for (int c = 0; c < CFG_COUNT; ++c) {
@@ -48,24 +50,30 @@ Plan make_plan(int dtype, bool mixed, int64_t M, int64_t N, int64_t K) {
     if (c < CFG_128x128 && (dtype != MAO_BF16 || mixed)) continue;
     const Shape& h = kShapes[c];
     const int64_t tm = ceil_div(M, h.bm), tn = ceil_div(N, h.bn), tiles = tm * tn;
-    const int64_t slots = 256 * h.per_cu;
-    const double rate = (dtype != MAO_BF16 ? kF32Rate[c == CFG_64x64] : h.rate) * 1e6 / h.per_cu;
+    const int per_cu = dtype != MAO_BF16 && c == CFG_64x64 ? 4 : h.per_cu;
+    const int slots = 256 * per_cu;
+    const double rate = (dtype != MAO_BF16 ? kF32Rate[c == CFG_64x64] : h.rate) * 1e6 / per_cu;
     const double slice_us = 2.0 * h.bm * h.bn * ks / rate;
     // parts of at least two slices, no more than 32, and only where a round is
     // not full without them
-    const int64_t most =
-        tiles >= slots ? 1 : std::min<int64_t>({32, slices / 2, ceil_div(2 * slots, tiles)});
-    for (int64_t s = 1; s <= std::max<int64_t>(1, most); ++s) {
-      const int64_t wgs = tiles * s, last = wgs % slots;
-      double one = ceil_div(slices, s) * slice_us;
-      const int64_t there = std::min<int64_t>(h.per_cu, ceil_div(wgs, 256));
-      one *= pow((double)there / h.per_cu, 0.6);
-      double us = (one + h.ends) * ((double)(wgs / slots) + (last ? 0.62 + 0.38 * last / slots : 0.0));
-      if (s > 1) us += 4.5 + 8.0 * s * M * N / 9e6;
+    const int most = tiles >= slots
+                         ? 1
+                         : std::max(1, std::min({32, slices / 2, (int)ceil_div(2 * slots, tiles)}));
+    for (int s = 1; s <= most; ++s) {
+      double one = ((slices + s - 1) / s) * slice_us, rounds;
+      if (s == 1 && tiles >= slots) {
+        const int64_t last = tiles % slots;
+        rounds = (double)(tiles / slots) + (last ? 0.7 + 0.3 * last / slots : 0.0);
+      } else {
+        const int wgs = (int)tiles * s, last = wgs % slots;
+        one *= kShare[per_cu][std::min(per_cu, (wgs + 255) / 256) - 1];
+        rounds = wgs / slots + (last ? 0.7 + 0.3 * last / slots : 0.0);
+      }
+      const double us = (one + h.ends) * rounds + (s > 1 ? 4.8 + part_us * s : 0.0);
       if (best_us == 0.0 || us < best_us) {
         best_us = us;
         best.cfg = c;
-        best.split = (int)s;
+        best.split = s;
         best.tiles_m = tm;
         best.tiles_n = tn;
         best.slices = slices;
@@ -76,10 +84,27 @@ Plan make_plan(int dtype, bool mixed, int64_t M, int64_t N, int64_t K) {
   return best;
 }
 
+// The last cuts of this thread, by size: an estimate takes about a microsecond of
+// host time, and a call needs it up to three times.
+Plan make_plan(int dtype, bool mixed, int64_t M, int64_t N, int64_t K) {
+  struct Entry {
+    int64_t M, N, K;
+    int type;
+    Plan plan;
+  };
+  static thread_local Entry memo[16] = {};
+  const int type = 1 + 2 * dtype + (mixed ? 1 : 0);  // 0: empty
+  Entry& e = memo[(uint64_t)(M * 31 + N * 17 + K * 7 + type) % 16];
+  if (e.type != type || e.M != M || e.N != N || e.K != K)
+    e = Entry{M, N, K, type, estimate_plan(dtype, mixed, M, N, K)};
+  return e.plan;
+}
+
 }  // namespace
 
 size_t lin_workspace(int dtype, int64_t M, int64_t N, int64_t K) {
   // the caller may not know the result types yet
+  if (dtype != MAO_BF16) return make_plan(dtype, false, M, N, K).ws;
   return std::max(make_plan(dtype, false, M, N, K).ws, make_plan(dtype, true, M, N, K).ws);
 }
 

@@ -784,7 +784,7 @@ mao_status pick(int dtype, int cfg, bool bf, const LinArgs& a, hipStream_t s) {
     case CFG_128x192: return go<Cfg<bf16_t, AKM, BKM, 128, 192, 2, 2, 128, 2, 2>, KIND, BF>(a, s);
     case CFG_192x128: return go<Cfg<bf16_t, AKM, BKM, 192, 128, 2, 2, 128, 2, 2>, KIND, BF>(a, s);
   }
-  if (cfg == CFG_64x64) return go<Cfg<bf16_t, AKM, BKM, 64, 64, 2, 2, 128, 2, 4>, KIND, false>(a, s);
+  if (cfg == CFG_64x64) return go<Cfg<bf16_t, AKM, BKM, 64, 64, 2, 2, 128, 3, 3>, KIND, false>(a, s);
   if (BF && bf) return go<Cfg<bf16_t, AKM, BKM, 128, 128, 2, 2, 128, 2, 2>, KIND, BF>(a, s);
   return go<Cfg<bf16_t, AKM, BKM, 128, 128, 2, 2, 128, 2, 2>, KIND, false>(a, s);
 }
