@@ -556,10 +556,12 @@ def _act(act):
 
 def q8_quantize(X, fmt="int8", out=None) -> Q8:
     """Keeps X (bf16 or fp32) in 8 bits."""
-    if out is None:
-        out = q8_empty(X.shape[0], X.shape[1], fmt, X.device)
-    _run("q8_quantize", X, out.codes, out.scales)
-    return out
+    if out is not None:
+        _run("q8_quantize", X, 0, out.codes, out.scales)
+        return out
+    q = Q8.__new__(Q8)
+    q.codes, q.scales = _run("q8_quantize", X, Q8_FORMATS[fmt], None, None)
+    return q
 
 
 def q8_dequantize(q: Q8, act="none", dtype=None, out=None):

@@ -220,14 +220,27 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (X, codes, scales, device, stream)
+// (X, format, codes, scales, device, stream) -> (codes, scales); new ones where None
 PyObject* q8_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 5, [&]() -> PyObject* {
-    const int64_t dev = integer(a[3]);
-    const mao_mat x = view(tensor(a[0]), dev);
-    const mao_q8 q = checkpoint(tensor(a[1]), tensor(a[2]), dev);
-    check(mao_q8_quantize(x, &q, (void*)integer(a[4])), "mao_q8_quantize");
-    Py_RETURN_NONE;
+  return guarded(n, 6, [&]() -> PyObject* {
+    const int64_t dev = integer(a[4]);
+    const at::Tensor& X = tensor(a[0]);
+    const mao_mat x = view(X, dev);
+    const int64_t blocks = (x.cols + 31) / 32;
+    at::Tensor codes, scales;
+    if (a[2] != Py_None) {
+      codes = tensor(a[2]);
+      scales = tensor(a[3]);
+    } else {
+      codes = at::empty({x.rows, blocks * 32},
+                        X.options().dtype(integer(a[1]) == MAO_Q8_INT8 ? at::kChar
+                                                                       : at::kFloat8_e4m3fn))
+                  .narrow(1, 0, x.cols);
+      scales = at::empty({x.rows, blocks}, X.options().dtype(at::kByte));
+    }
+    const mao_q8 q = checkpoint(codes, scales, dev);
+    check(mao_q8_quantize(x, &q, (void*)integer(a[5])), "mao_q8_quantize");
+    return Py_BuildValue("NN", wrap(codes, a[2]), wrap(scales, a[2] == Py_None ? Py_None : a[3]));
   });
 }
 

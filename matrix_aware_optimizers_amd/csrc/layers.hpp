@@ -172,7 +172,7 @@ int lin_sum_rows(int dtype, int64_t M, int64_t N, int64_t K);
 mao_status launch_linear(int dtype, const LinProblem& p, void* ws, float* sums, hipStream_t s);
 
 // Up to kTokenRows rows of X against W (N x K), both K-contiguous.
-constexpr int kTokenRows = 64;
+constexpr int kTokenRows = 16;
 mao_status launch_linear_token(int dtype, const LinProblem& p, hipStream_t s);
 
 }  // namespace mao

@@ -1,13 +1,15 @@
-// The linear layer's forward product for a few rows (decoded tokens, short
-// prompts): y = act(x W^T + b) + res with up to 64 rows of x.
+// The linear layer's forward product for up to 16 rows (decoded tokens): y = act(x W^T
+// + b) + res.
 //
-// Bound: reading W once. A workgroup takes 16 rows of W and all of K; its
-// wavefronts take 256-byte blocks of those rows in turn, straight from memory
-// into registers in the MFMA operand layout (16 x 16 results: W rows x tokens,
-// so a wavefront's load is 64 contiguous bytes of each of 16 rows), the next
-// block requested before the current one is multiplied. x is small and comes
-// from L2. The wavefronts' sums are joined through LDS in a fixed order and the
-// first wavefronts finish the result.
+// Bound: reading W once (1536 -> 6144 bf16 6.3 us, 3.6 of them the bytes at the copy
+// rate, the rest the launch: 512 -> 512 takes 3.7; 4096 -> 14336 22.4 us, the copy
+// rate). A workgroup takes 16 rows of W and all of K; its wavefronts take 256-byte
+// blocks of those rows in turn, straight from memory into registers in the MFMA
+// operand layout (16 x 16 results: W rows x tokens, so a wavefront's load is 64
+// contiguous bytes of each of 16 rows), the next block requested before the current
+// one is multiplied. x is small and comes from L2; with more rows reading it again
+// for every 16 rows of W costs more than the tile kernels do (60 rows, 6144 -> 1536:
+// 28 us). The wavefronts' sums are joined through LDS in a fixed order.
 #include "act.hpp"
 #include "layers.hpp"
 
@@ -21,22 +23,17 @@ constexpr int kStep = 64;      // bytes of a row per MFMA step
 constexpr int kSteps = 4;      // steps per block
 constexpr int kBlockBytes = kStep * kSteps;
 
-template <typename T, int FT>
-__device__ __forceinline__ void mma16(const uint4& w, const uint4 (&x)[FT], f32x4_t (&acc)[FT]) {
+template <typename T>
+__device__ __forceinline__ void mma16(const uint4& w, const uint4& x, f32x4_t& acc) {
+  if constexpr (sizeof(T) == 2) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w),
+                                                  __builtin_bit_cast(bf16x8_t, x), acc, 0, 0, 0);
+  } else {
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w}, b[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-  for (int f = 0; f < FT; ++f) {
-    if constexpr (sizeof(T) == 2) {
-      acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w),
-                                                       __builtin_bit_cast(bf16x8_t, x[f]), acc[f],
-                                                       0, 0, 0);
-    } else {
-      const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-      const uint32_t b[4] = {x[f].x, x[f].y, x[f].z, x[f].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        acc[f] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[e]), __uint_as_float(b[e]),
-                                                      acc[f], 0, 0, 0);
-    }
+    for (int e = 0; e < 4; ++e)
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[e]), __uint_as_float(b[e]), acc,
+                                                 0, 0, 0);
   }
 }
 
@@ -59,31 +56,25 @@ __device__ __forceinline__ uint4 load_masked(const T* row, int k, int K) {
   return u.v;
 }
 
-template <typename T, int FT, int WAVES>
+template <typename T, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void linear_token_kernel(LinProblem P) {
   constexpr int EPC = 16 / (int)sizeof(T), KSTEP = kStep / (int)sizeof(T);
   constexpr int KBLK = KSTEP * kSteps;
-  __shared__ __attribute__((aligned(16))) float red[WAVES][FT][256];
+  __shared__ __attribute__((aligned(16))) float red[WAVES][256];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, q = lane >> 4;
   const int n0 = blockIdx.x * 16;
   const T* wrow = (const T*)P.B + (int64_t)min(n0 + r, P.N - 1) * P.ldb;
-  const T* xrow[FT];
-#pragma unroll
-  for (int f = 0; f < FT; ++f)
-    xrow[f] = (const T*)P.A + (int64_t)min(16 * f + r, P.M - 1) * P.lda;
-  f32x4_t acc[FT];
-#pragma unroll
-  for (int f = 0; f < FT; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const T* xrow = (const T*)P.A + (int64_t)min(r, P.M - 1) * P.lda;
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
 
-  uint4 w[2][kSteps], x[2][kSteps][FT];
+  uint4 w[2][kSteps], x[2][kSteps];
   auto load = [&](int b, int s) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       const int k = b * KBLK + i * KSTEP + q * EPC;
       w[s][i] = *(const uint4*)(wrow + k);
-#pragma unroll
-      for (int f = 0; f < FT; ++f) x[s][i][f] = *(const uint4*)(xrow[f] + k);
+      x[s][i] = *(const uint4*)(xrow + k);
     }
   };
   const int nb = P.K / KBLK;
@@ -92,37 +83,30 @@ __global__ __launch_bounds__(64 * WAVES) void linear_token_kernel(LinProblem P) 
   while (b < nb) {
     if (b + WAVES < nb) load(b + WAVES, 1);
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) mma16<T, FT>(w[0][i], x[0][i], acc);
+    for (int i = 0; i < kSteps; ++i) mma16<T>(w[0][i], x[0][i], acc);
     b += WAVES;
     if (b >= nb) break;
     if (b + WAVES < nb) load(b + WAVES, 0);
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) mma16<T, FT>(w[1][i], x[1][i], acc);
+    for (int i = 0; i < kSteps; ++i) mma16<T>(w[1][i], x[1][i], acc);
     b += WAVES;
   }
   // steps past the last whole block, one per wavefront in turn
   const int k1 = nb * KBLK;
   for (int t = wave; k1 + t * KSTEP < P.K; t += WAVES) {
     const int k = k1 + t * KSTEP + q * EPC;
-    const uint4 wv = load_masked(wrow, k, P.K);
-    uint4 xv[FT];
-#pragma unroll
-    for (int f = 0; f < FT; ++f) xv[f] = load_masked(xrow[f], k, P.K);
-    mma16<T, FT>(wv, xv, acc);
+    mma16<T>(load_masked(wrow, k, P.K), load_masked(xrow, k, P.K), acc);
   }
-#pragma unroll
-  for (int f = 0; f < FT; ++f)
-    *(float4*)&red[wave][f][lane * 4] = make_float4(acc[f][0], acc[f][1], acc[f][2], acc[f][3]);
+  *(float4*)&red[wave][lane * 4] = make_float4(acc[0], acc[1], acc[2], acc[3]);
   __syncthreads();
-  // thread (f, lane'): columns n0 + 4 (lane' / 16) + 0..3 of row 16 f + lane' % 16
-  for (int u = threadIdx.x; u < FT * 64; u += 64 * WAVES) {
-    const int f = u >> 6, l = u & 63;
-    const int row = 16 * f + (l & 15), col = n0 + 4 * (l >> 4);
-    if (row >= P.M || col >= P.N) continue;
+  // the first wavefront: lane l has columns n0 + 4 (l / 16) + 0..3 of row l % 16
+  if (wave == 0) {
+    const int row = r, col = n0 + 4 * q;
+    if (row >= P.M || col >= P.N) return;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < WAVES; ++k) {
-      const float4 t = *(const float4*)&red[k][f][l * 4];
+      const float4 t = *(const float4*)&red[k][lane * 4];
       v[0] += t.x;
       v[1] += t.y;
       v[2] += t.z;
@@ -163,31 +147,23 @@ __global__ __launch_bounds__(64 * WAVES) void linear_token_kernel(LinProblem P) 
   }
 }
 
-template <typename T, int FT>
+template <typename T>
 mao_status go(const LinProblem& p, hipStream_t s) {
   const dim3 grid((int)ceil_div(p.N, 16));
-  // wavefronts per workgroup: about three blocks of K each
-  const int64_t blocks = p.K / (kBlockBytes / (int)sizeof(T));
-  constexpr int WIDE = FT == 1 ? 16 : 8;  // more tokens need more registers
-  if (blocks >= 24)
-    hipLaunchKernelGGL((linear_token_kernel<T, FT, WIDE>), grid, dim3(64 * WIDE), 0, s, p);
+  // from 32 blocks of K on, eight wavefronts (bf16, one row: 4096 -> 14336 25.0 -> 22.4
+  // us); below, four (1536 -> 6144 6.3 against 6.4 us)
+  if (p.K / (kBlockBytes / (int)sizeof(T)) >= 32)
+    hipLaunchKernelGGL((linear_token_kernel<T, 8>), grid, dim3(512), 0, s, p);
   else
-    hipLaunchKernelGGL((linear_token_kernel<T, FT, 4>), grid, dim3(256), 0, s, p);
+    hipLaunchKernelGGL((linear_token_kernel<T, 4>), grid, dim3(256), 0, s, p);
   MAO_LAUNCH_CHECK();
   return MAO_OK;
-}
-
-template <typename T>
-mao_status pick(const LinProblem& p, hipStream_t s) {
-  if (p.M <= 16) return go<T, 1>(p, s);
-  if (p.M <= 32) return go<T, 2>(p, s);
-  return go<T, 4>(p, s);
 }
 
 }  // namespace
 
 mao_status launch_linear_token(int dtype, const LinProblem& p, hipStream_t s) {
-  return dtype == MAO_BF16 ? pick<bf16_t>(p, s) : pick<float>(p, s);
+  return dtype == MAO_BF16 ? go<bf16_t>(p, s) : go<float>(p, s);
 }
 
 }  // namespace mao
