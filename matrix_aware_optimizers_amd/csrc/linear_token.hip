@@ -1,15 +1,21 @@
 // The linear layer's forward product for up to 16 rows (decoded tokens): y = act(x W^T
 // + b) + res.
 //
-// Bound: reading W once (1536 -> 6144 bf16 6.3 us, 3.6 of them the bytes at the copy
-// rate, the rest the launch: 512 -> 512 takes 3.7; 4096 -> 14336 22.4 us, the copy
-// rate). A workgroup takes 16 rows of W and all of K; its wavefronts take 256-byte
-// blocks of those rows in turn, straight from memory into registers in the MFMA
-// operand layout (16 x 16 results: W rows x tokens, so a wavefront's load is 64
+// Bound: reading W once (one row, bf16: 1536 -> 6144 5.9 us, 3.6 of them the bytes at
+// the copy rate and the rest the launch, 512 -> 512 takes 3.7; 4096 -> 14336 22.3 us,
+// the copy rate). A workgroup takes 16 rows of W and all of K; its wavefronts take
+// 256-byte blocks of those rows in turn, straight from memory into registers in the
+// MFMA operand layout (16 x 16 results: W rows x tokens, so a wavefront's load is 64
 // contiguous bytes of each of 16 rows), the next block requested before the current
-// one is multiplied. x is small and comes from L2; with more rows reading it again
-// for every 16 rows of W costs more than the tile kernels do (60 rows, 6144 -> 1536:
-// 28 us). The wavefronts' sums are joined through LDS in a fixed order.
+// one is multiplied. x is small and comes from L2. The wavefronts' sums are joined
+// through LDS in a fixed order.
+//
+// 16 rows fill one MFMA result; the tile kernels take the rest. Timed against them
+// (this kernel : tiles, us, bf16): 1536 -> 6144 1 row 5.9 : 11.4, 16 rows 7.5 : 11.4;
+// 6144 -> 1536 8.9 : 10.7 and 12.7 : 11.5; 4096 -> 14336 22.3 : 39.2 and 33.3 : 39.5.
+// Several results a wavefront, for up to 64 rows, read x again for every 16 rows of W:
+// 32 rows 10.5 : 11.5, 18.5 : 11.3 and 52 : 40, 60 rows 17 : 12, 28 : 12 and 80 : 40.
+// It won only between 17 and about 32 rows of the first of these shapes.
 #include "act.hpp"
 #include "layers.hpp"
 
