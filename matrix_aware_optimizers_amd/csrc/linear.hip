@@ -14,62 +14,68 @@ struct Plan {
   size_t ws;
 };
 
-// Tile shapes: workgroups per CU, TFLOP/s of a CU full of them (bf16, long K) and
-// the microseconds a workgroup takes to start and to finish its result.
+// Tile shapes: workgroups that share a CU, TFLOP/s of a CU full of them (long K), the
+// microseconds a workgroup takes to start and to finish its result, and the time of
+// o = 1, 2, .. workgroups on a CU relative to a full one's.
 struct Shape {
   int bm, bn, per_cu;
-  double rate, ends;
+  double rate, ends, share[4];
 };
 const Shape kShapes[CFG_COUNT] = {
-    {256, 256, 1, 5.43, 11.4}, {256, 192, 1, 4.95, 8.6}, {128, 192, 2, 5.2, 9.7},
-    {192, 128, 2, 5.2, 9.1},   {128, 128, 2, 4.2, 6.9},  {64, 64, 3, 2.5, 4.9},
+    {256, 256, 1, 5.54, 12.4, {1.0}},        {256, 192, 1, 4.79, 8.16, {1.0}},
+    {192, 128, 2, 4.34, 9.61, {0.802, 1.0}}, {128, 128, 2, 4.01, 6.80, {0.907, 1.0}},
+    {64, 64, 3, 2.03, 4.18, {0.556, 0.805, 1.0}},
 };
-constexpr double kF32Rate[2] = {0.485, 0.53};  // 128 x 128 and 64 x 64 tiles
+const Shape kShapesF32[2] = {  // CFG_128x128, CFG_64x64
+    {128, 128, 2, 0.476, 5.33, {0.511, 1.0}},
+    {64, 64, 4, 0.546, 1.66, {0.339, 0.582, 0.799, 1.0}},
+};
+constexpr double kLastRound = 0.91;     // of a round's time for a last one nearly empty
+constexpr double kJoinUs = 3.16;        // launch of the join
+constexpr double kPartPerUs = 4.61e6;   // bytes of partial results written and read per us
 
 // The cut with the shortest estimated time. Tiles run in rounds of 256 workgroups
 // times those that share a CU; a last round that is not full is shorter too (the
-// clock rises as CUs idle). Of p workgroups that fit a CU, o take the square root
-// of o / p of the time of p. With few tiles K is split: more workgroups, then a launch and one pass
-// over the partial results.
+// clock rises as CUs idle). With few tiles K is split: more workgroups, then a launch
+// and one pass over the partial results.
 //
-// The constants minimise the loss over 117 products (three layouts, both types, 77
-// to 16384 rows, K from 200 to 16384, operands not in the L2) timed with every shape
-// and up to 14 splits on MI355X: the estimate's choice is 2% slower than the best
-// one on average, 15% at worst (512 x 4096 x 4096, 40 against 35 us).
+// The constants are fitted to 888 products (296 drawn sizes, three layouts, both
+// types, 65 to 16384 rows, operands mostly not in the L2), each timed on MI355X with
+// the shapes and up to 14 splits. On sizes drawn apart, which they were not fitted
+// to, the estimate's choice is 1.8% slower than the best one timed on average over
+// 252 small and middle products and 28.8% at worst (dW of 2759 rows, 7689 -> 79: 29.2
+// against 22.6 us), 1.4% and 12.4% over 48 products of 1e11 to 1e12
+// multiply-adds. Constants fitted to 38 chosen sizes lost 1.2% on those and
+// 4.1% (32.5% at worst) and 4.6% (22.2%) on these.
+// The same draws on what a shape is worth, in bf16 products of 1e11 multiply-adds and
+// more: without 256 x 192 tiles they lose 3.0% (sizes drawn apart) and 3.1% (sizes
+// fitted to) instead of 1.4% and 2.0%; without 192 x 128 1.4% and 2.4%. 128 x 192
+// beside it gained nothing and is not built.
 Plan estimate_plan(int dtype, bool mixed, int64_t M, int64_t N, int64_t K) {
-  // sqrt(o / p) for o = 1 .. p
-  static const double kShare[5][4] = {
-      {}, {1.0}, {0.707, 1.0}, {0.577, 0.816, 1.0}, {0.5, 0.707, 0.866, 1.0}};
   const int ks = dtype == MAO_BF16 ? 64 : 32;
   const int slices = (int)ceil_div(K, ks);
-  const double part_us = 8.0 * M * N / 1e7;
+  const double part_us = 8.0 * M * N / kPartPerUs;
   Plan best = {};
   double best_us = 0.0;
   for (int c = 0; c < CFG_COUNT; ++c) {
     // fp32 operands and mixed result types come with the small square tiles only
     if (c < CFG_128x128 && (dtype != MAO_BF16 || mixed)) continue;
-    const Shape& h = kShapes[c];
+    const Shape& h = dtype == MAO_BF16 ? kShapes[c] : kShapesF32[c - CFG_128x128];
     const int64_t tm = ceil_div(M, h.bm), tn = ceil_div(N, h.bn), tiles = tm * tn;
-    const int per_cu = dtype != MAO_BF16 && c == CFG_64x64 ? 4 : h.per_cu;
-    const int slots = 256 * per_cu;
-    const double rate = (dtype != MAO_BF16 ? kF32Rate[c == CFG_64x64] : h.rate) * 1e6 / per_cu;
-    const double slice_us = 2.0 * h.bm * h.bn * ks / rate;
+    const int slots = 256 * h.per_cu;
+    const double slice_us = 2.0 * h.bm * h.bn * ks * h.per_cu / (h.rate * 1e6);
     // parts of at least two slices, no more than 32, and only where a round is
     // not full without them
     const int most = tiles >= slots
                          ? 1
                          : std::max(1, std::min({32, slices / 2, (int)ceil_div(2 * slots, tiles)}));
     for (int s = 1; s <= most; ++s) {
-      double one = ((slices + s - 1) / s) * slice_us, rounds;
-      if (s == 1 && tiles >= slots) {
-        const int64_t last = tiles % slots;
-        rounds = (double)(tiles / slots) + (last ? 0.7 + 0.3 * last / slots : 0.0);
-      } else {
-        const int wgs = (int)tiles * s, last = wgs % slots;
-        one *= kShare[per_cu][std::min(per_cu, (wgs + 255) / 256) - 1];
-        rounds = wgs / slots + (last ? 0.7 + 0.3 * last / slots : 0.0);
-      }
-      const double us = (one + h.ends) * rounds + (s > 1 ? 4.8 + part_us * s : 0.0);
+      const int64_t wgs = tiles * s, last = wgs % slots;
+      const int here = (int)std::min<int64_t>(h.per_cu, ceil_div(wgs, 256));
+      const double one = ((slices + s - 1) / s) * slice_us * h.share[here - 1] + h.ends;
+      const double rounds = (double)(wgs / slots) +
+                            (last ? kLastRound + (1.0 - kLastRound) * last / slots : 0.0);
+      const double us = one * rounds + (s > 1 ? kJoinUs + part_us * s : 0.0);
       if (best_us == 0.0 || us < best_us) {
         best_us = us;
         best.cfg = c;

@@ -18,8 +18,7 @@ mao_status launch_linear_join(const LinProblem& p, const float* part, int64_t ld
                               bool slope, hipStream_t s);
 
 // Tile configurations (linear_tile.hpp).
-enum { CFG_256x256 = 0, CFG_256x192, CFG_128x192, CFG_192x128, CFG_128x128, CFG_64x64,
-       CFG_COUNT };
+enum { CFG_256x256 = 0, CFG_256x192, CFG_192x128, CFG_128x128, CFG_64x64, CFG_COUNT };
 
 // One translation unit per product: linear_fwd.hip, linear_dx.hip, linear_dw.hip.
 // bf: every tensor of the epilogue but a checkpoint is bf16.

@@ -10,8 +10,9 @@
 // transposing read (ds_read_b64_tr_b16), fp32 ones by single elements, whose
 // MFMA (32x32x2) takes one element per lane anyway.
 //
-// A workgroup of 4 wavefronts (2 x 2) computes a BM x BN tile, each wavefront
-// (BM/2) x (BN/2) as 32 x 32 MFMA blocks, fp32 accumulation. K advances in
+// A workgroup of 4 wavefronts (2 x 2), or 8 (4 x 2) for the tiles of 256 rows,
+// computes a BM x BN tile, each wavefront its share of it as 32 x 32 MFMA blocks,
+// fp32 accumulation. K advances in
 // slices of KSB bytes per row, copied global -> LDS without staging registers
 // into a ring of NST stages. One barrier per slice: before it every wavefront
 // has read its last fragments of slice k and waited for its loads of slice
@@ -309,15 +310,12 @@ struct Cfg {
   static constexpr int JU = FN % 2 == 0 ? 2 : FN;
   static constexpr int PIECE = 32 * piece_ld(JU) * 4;
   static_assert(AB % (16 * THREADS) == 0 && BB % (16 * THREADS) == 0, "whole loads per thread");
-  static_assert(NST >= 2 && NST <= 4, "ring stages");
+  static_assert(NST == 2 || NST == 3, "ring stages");
   static_assert(WAVES / 2 * PIECE + BN * 4 <= STAGE, "the epilogue's pieces and the bias fit the stages");
 };
 
-// XOR permutation of a K-contiguous row's 16-byte chunks.
-template <int KSB>
-__device__ __forceinline__ int swz_k(int row) {
-  return KSB == 128 ? (row >> 1) & 7 : ((row >> 1) ^ (row >> 2)) & 3;
-}
+// XOR permutation of a K-contiguous row's 16-byte chunks (128 bytes per row).
+__device__ __forceinline__ int swz_k(int row) { return (row >> 1) & 7; }
 // XOR permutation of a K-major row's chunks (BX: tile rows of the operand).
 template <int BX, int ES>
 __device__ __forceinline__ int swz_m(int krow) {
@@ -346,13 +344,13 @@ struct Operand {
         const int col = x0 + (slot ^ swz_m<BX, ES>(r)) * EPC;
         src[q] = p + (int64_t)r * ld + min(col, (X - 1) / EPC * EPC);
       } else {
-        src[q] = p + (int64_t)min(x0 + r, X - 1) * ld + (slot ^ swz_k<KSB>(r)) * EPC;
+        src[q] = p + (int64_t)min(x0 + r, X - 1) * ld + (slot ^ swz_k(r)) * EPC;
       }
     }
     if constexpr (!KM) {
       const int r = w * (BX / WX) + r32;
 #pragma unroll
-      for (int s = 0; s < SUB; ++s) frag[s] = r * KSB + (((2 * s + h) ^ swz_k<KSB>(r)) << 4);
+      for (int s = 0; s < SUB; ++s) frag[s] = r * KSB + (((2 * s + h) ^ swz_k(r)) << 4);
     } else if constexpr (ES == 2) {
       const int ti = lane & 15, tg = (lane >> 4) & 1;
       const int krow = 8 * h + (ti >> 2);
@@ -398,7 +396,7 @@ struct Operand {
           for (int i = 0; i < EPC; ++i)
             if (col + i < X) u.e[i] = p[k * ld + col + i];
       } else {
-        const int64_t k = k0 + (slot ^ swz_k<KSB>(r)) * EPC;
+        const int64_t k = k0 + (slot ^ swz_k(r)) * EPC;
         if (x0 + r < X)
           for (int i = 0; i < EPC; ++i)
             if (k + i < kend) u.e[i] = p[(int64_t)(x0 + r) * ld + k + i];
@@ -437,7 +435,6 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void linear_tile_kernel(LinArgs
   __shared__ __attribute__((aligned(16))) unsigned char st0[C::STAGE];
   __shared__ __attribute__((aligned(16))) unsigned char st1[C::STAGE];
   __shared__ __attribute__((aligned(16))) unsigned char st2[NST > 2 ? C::STAGE : 16];
-  __shared__ __attribute__((aligned(16))) unsigned char st3[NST > 3 ? C::STAGE : 16];
 
   // Workgroups reach the 8 XCDs round-robin: each XCD takes a contiguous run of
   // the (split, tile) list, neighbours sharing panels in its L2.
@@ -657,7 +654,6 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void linear_tile_kernel(LinArgs
     issue(st0, 0);
     if (nk > 1) issue(st1, 1);
     if (NST > 2 && nk > 2) issue(st2, 2);
-    if (NST > 3 && nk > 3) issue(st3, 3);
     // wait for slice 0
     if (nk >= NST)
       wait_slice<(NST - 1) * LPT>();
@@ -675,7 +671,7 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void linear_tile_kernel(LinArgs
         step(st1, st0, k + 1);
       }
       if (k < nk) step(st0, st1, k);
-    } else if constexpr (NST == 3) {
+    } else {
       for (; k + 3 <= nk; k += 3) {
         step(st0, st1, k);
         step(st1, st2, k + 1);
@@ -683,16 +679,6 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void linear_tile_kernel(LinArgs
       }
       if (k < nk) step(st0, st1, k);
       if (k + 1 < nk) step(st1, st2, k + 1);
-    } else {
-      for (; k + 4 <= nk; k += 4) {
-        step(st0, st1, k);
-        step(st1, st2, k + 1);
-        step(st2, st3, k + 2);
-        step(st3, st0, k + 3);
-      }
-      if (k < nk) step(st0, st1, k);
-      if (k + 1 < nk) step(st1, st2, k + 1);
-      if (k + 2 < nk) step(st2, st3, k + 2);
     }
   }
   // every wavefront is past the last slice's barrier: no LDS reads or loads
@@ -781,7 +767,6 @@ mao_status pick(int dtype, int cfg, bool bf, const LinArgs& a, hipStream_t s) {
   switch (cfg) {
     case CFG_256x256: return go<Cfg<bf16_t, AKM, BKM, 256, 256, 4, 2, 128, 2, 2>, KIND, BF>(a, s);
     case CFG_256x192: return go<Cfg<bf16_t, AKM, BKM, 256, 192, 4, 2, 128, 2, 2>, KIND, BF>(a, s);
-    case CFG_128x192: return go<Cfg<bf16_t, AKM, BKM, 128, 192, 2, 2, 128, 2, 2>, KIND, BF>(a, s);
     case CFG_192x128: return go<Cfg<bf16_t, AKM, BKM, 192, 128, 2, 2, 128, 2, 2>, KIND, BF>(a, s);
   }
   if (cfg == CFG_64x64) return go<Cfg<bf16_t, AKM, BKM, 64, 64, 2, 2, 128, 3, 3>, KIND, false>(a, s);

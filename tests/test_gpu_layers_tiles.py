@@ -55,6 +55,7 @@ FWD = [(123, 77, 88), (104, 790, 68), (674, 344, 5453), (5621, 3205, 141), (938,
        (133, 5185, 2774), (455, 5113, 4167), (67, 1896, 87)]
 FWD += [(585, 65, 4933), (616, 3431, 838), (2899, 130, 4147), (430, 3523, 2697), (644, 565, 5400),
         (653, 3235, 1798), (391, 5645, 3255), (645, 5125, 5581)]
+FWD += [(4383, 102, 5508), (517, 5000, 5158), (4448, 4777, 581)]
 FWD32 = [(1545, 69, 2634), (3685, 1335, 1129), (123, 77, 88), (77, 468, 143)]
 FWD32 += [(8410, 845, 462), (91, 343, 98)]
 
@@ -84,6 +85,7 @@ DX = [(123, 77, 88), (142, 82, 883), (2219, 1994, 325), (910, 1305, 4768), (4987
       (131, 2815, 5189), (454, 4171, 5030), (2148, 5484, 72), (96, 76, 1655)]
 DX += [(680, 4439, 70), (1377, 332, 3406), (404, 2699, 3289), (1038, 3718, 537), (660, 1868, 3233),
     (385, 3369, 5645), (659, 5454, 5553), (65, 98, 1493)]
+DX += [(2907, 4048, 265), (3441, 1738, 5956), (3687, 652, 5065)]
 DX32 = [(2474, 1800, 82), (723, 5954, 1337), (123, 77, 88), (69, 85, 424)]
 DX32 += [(964, 4217, 946), (66, 104, 313)]
 
@@ -113,6 +115,7 @@ DW = [(123, 77, 88), (1254, 90, 67), (338, 4623, 780), (4485, 1324, 908), (336, 
       (3572, 1234, 1041), (67, 5065, 1559), (5736, 1723, 1233), (8257, 2391, 1176), (1612, 104, 81)]
 DW += [(68, 1218, 2462), (4012, 1784, 195), (65, 5676, 2138), (3318, 2720, 389), (461, 3096, 1289),
     (3363, 1166, 1060), (4106, 546, 3658), (6338, 2372, 1200)]
+DW += [(6086, 4453, 618), (376, 2150, 5641), (6930, 4925, 530)]
 DW32 = [(65, 1389, 2993), (1422, 975, 4199), (123, 77, 88), (428, 81, 85)]
 DW32 += [(939, 902, 4419)]
 
