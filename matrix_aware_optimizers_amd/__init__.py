@@ -2,8 +2,9 @@
 and the layer operators that make their gradients (layer norm, linear layer,
 8-bit activation checkpoints).
 
-Thin ctypes binding over ``libmao.so`` (declared in ``include/mao.h``). The
-binding only marshals arguments: every step runs in the library's HIP
+Thin binding over ``libmao.so`` (declared in ``include/mao.h``): ctypes for the
+steps, the C++ extension ``_layers.so`` for the layer operators. The binding only
+marshals arguments: every step runs in the library's HIP
 kernels, on the current torch stream. PyTorch provides device memory and
 streams; the library itself allocates nothing, so the workspace is a torch
 byte tensor allocated here and cached per device.

