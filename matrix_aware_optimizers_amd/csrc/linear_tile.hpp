@@ -38,13 +38,14 @@
 // results go to the workspace, and a second launch (linear_join.hip) adds them
 // in a fixed order and finishes the result. No atomics anywhere.
 //
-// Bound: matrix cores for thousands of rows, and there the clock the card holds under
-// them (1.7 to 2 GHz); the activation's arithmetic of a 256 x 256 tile, about 10 us, is
-// not hidden, one workgroup of such tiles fills a CU. Measured (MI355X, bf16): 16384
-// rows 1536 -> 6144 with bias, gelu and its pre-activation kept 323 us, 958 TFLOP/s;
-// the input gradient of 6144 -> 1536 with the slope from int8 codes 353 us, 876; dW of
-// 8191 rows 14336 -> 4096 (the product alone) 879 us, 1094. The ROCm library's bare
-// bf16 products of these sizes reach 1121, 1138 and 973.
+// Bound: matrix cores for thousands of rows, plus a result's way out, which nothing
+// hides: one workgroup of 256 x 256 tiles fills a CU, and every round ends in a burst
+// of stores. Measured (MI355X, bf16, 16384 rows): 1536 -> 6144 without epilogue 278 us,
+// 1110 TFLOP/s; keeping the pre-activation too adds 36 (201 MB written, 38 us at the
+// copy rate), gelu_tanh 15 (9 beside the stores of both). Input gradient of 6144 ->
+// 1536 271 us; reading int8 codes and relu's slope adds 25, gelu_tanh's 25 more. dW of
+// 8191 rows 14336 -> 4096 840 us, 1146 TFLOP/s. The ROCm library's bare products on
+// the same tensors: 214, 251 and 968 us.
 #pragma once
 
 #include "act.hpp"
