@@ -21,7 +21,7 @@
 // kernel 3.4 of them. Backward with a joining gradient 16384 x 1536 44.3 us
 // (34.4 and 4.2 for the partial rows; 201 MB, 5.9 TB/s over the first); 4093 x 4096
 // from int8 codes 25.9 us (24.4 are the kernel, 84 MB, 3.5 TB/s: 16 rows
-// per workgroup are too few to hide each row's two reductions). Rows above 8192
+// per workgroup are too few to hide each row's reduction, both sums in one exchange). Rows above 8192
 // columns hold two or four runs per thread and spill a few registers in the backward
 // pass.
 //
