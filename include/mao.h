@@ -522,8 +522,9 @@ MAO_API mao_status mao_linear_backward_input(mao_mat dY, mao_mat W, int32_t act,
  * mao_linear_backward_weight -- dW = dY^T a [+ dW];  dbias = sum over rows of dY
  * [+ dbias], with a = x_act(X) (rows x k). The layer's input is X (dY's dtype)
  * or its checkpoint X8 (exactly one); x_act recomputes an activation that was
- * not kept. Against a bf16 dY, a is rounded to bf16, as the forward product
- * read it (without x_act a checkpoint's values are exact in bf16). dW: n x k,
+ * not kept. Against a bf16 dY, a recomputed a enters a bf16 dW rounded to bf16,
+ * as the forward product read it, and an fp32 dW in two bf16 parts (16 bits of
+ * it) by two products (without x_act a checkpoint's values are exact in bf16). dW: n x k,
  * bf16 or fp32; dbias: NULL or n floats. accumulate != 0 adds to both (the
  * micro-batches of one step).
  */

@@ -598,7 +598,9 @@ def linear_backward_input(dY, W, *, act="none", preact=None, add=None, out=None)
 def linear_backward_weight(dY, X, *, x_act="none", dtype=None, out=None, dbias=None,
                            accumulate=False):
     """(dW, dbias) = (dY^T x_act(X), column sums of dY), dW in fp32 unless ``dtype``
-    or ``out`` says bf16. X: the layer's input or its Q8 checkpoint. With
+    or ``out`` says bf16. X: the layer's input or its Q8 checkpoint. With a bf16 dY,
+    a recomputed activation costs an fp32 dW a second product (it holds 16 bits of
+    the activation; a bf16 dW takes it rounded to bf16). With
     ``accumulate`` both are added to ``out`` and ``dbias``, which then have to be
     given."""
     if accumulate and (out is None or dbias is None):

@@ -132,12 +132,14 @@ mao_status launch_partial_sum(const float* part, int64_t stride, int blocks, int
 // ---- 8-bit checkpoints (q8.hip) --------------------------------------------
 mao_status launch_q8_quantize(const void* x, int dtype, int64_t ldx, int rows, int cols, Q8View q,
                               int fmt, hipStream_t s);
-mao_status launch_q8_dequantize(Q8View q, int fmt, int rows, int cols, int act, void* y, int dtype,
-                                int64_t ldy, hipStream_t s);
+// rest: what rounding to bf16 leaves of each value instead of the value (0 where that
+// rounding is not finite), so that value and rest together carry 16 bits of it.
+mao_status launch_q8_dequantize(Q8View q, int fmt, int rows, int cols, int act, bool rest, void* y,
+                                int dtype, int64_t ldy, hipStream_t s);
 
-// y = act(x), one dtype
-mao_status launch_act(const void* x, int dtype, int64_t ldx, int rows, int cols, int act, void* y,
-                      int64_t ldy, hipStream_t s);
+// y = act(x) or its rest, one dtype
+mao_status launch_act(const void* x, int dtype, int64_t ldx, int rows, int cols, int act, bool rest,
+                      void* y, int64_t ldy, hipStream_t s);
 
 // ---- linear layer (linear.hip, linear_token.hip) ---------------------------
 // What happens to a result before it is stored:

@@ -138,8 +138,8 @@ mao_status mao_q8_dequantize(const mao_q8* X8, int32_t act, mao_mat Y, void* str
   b.out(range_of(Y));
   b.in(X8);
   MAO_TRY(b.check());
-  return launch_q8_dequantize(view_of(*X8), X8->format, (int)Y.rows, (int)Y.cols, act, Y.data,
-                              Y.dtype, Y.ld, (hipStream_t)stream);
+  return launch_q8_dequantize(view_of(*X8), X8->format, (int)Y.rows, (int)Y.cols, act, false,
+                              Y.data, Y.dtype, Y.ld, (hipStream_t)stream);
 }
 
 mao_status mao_layer_norm(mao_mat X, const void* gamma, const void* beta, int32_t param_dtype,
@@ -408,12 +408,15 @@ mao_status mao_linear_backward_weight(mao_mat dY, const mao_mat* X, const mao_q8
   p.M = (int)dW.rows;
   p.N = (int)dW.cols;
   p.K = (int)dY.rows;
+  // the input (or what its rounding to bf16 left) into the workspace
+  auto rebuild = [&](bool rest) {
+    return X8 ? launch_q8_dequantize(view_of(*X8), X8->format, (int)X8->rows, (int)X8->cols, x_act,
+                                     rest, w.x, dY.dtype, w.ldx, s)
+              : launch_act(X->data, X->dtype, X->ld, (int)X->rows, (int)X->cols, x_act, rest, w.x,
+                           w.ldx, s);
+  };
   if (rebuilt) {
-    if (X8)
-      MAO_TRY(launch_q8_dequantize(view_of(*X8), X8->format, (int)X8->rows, (int)X8->cols, x_act,
-                                   w.x, dY.dtype, w.ldx, s));
-    else
-      MAO_TRY(launch_act(X->data, X->dtype, X->ld, (int)X->rows, (int)X->cols, x_act, w.x, w.ldx, s));
+    MAO_TRY(rebuild(false));
     p.B = w.x;
     p.ldb = w.ldx;
   } else {
@@ -429,6 +432,20 @@ mao_status mao_linear_backward_weight(mao_mat dY, const mao_mat* X, const mao_q8
     p.e.add_dtype = dW.dtype;
   }
   MAO_TRY(launch_linear(dY.dtype, p, w.part, dbias ? w.sums : nullptr, s));
+  // bf16 matrix cores take a recomputed activation rounded to bf16. Into an fp32 dW
+  // what that rounding left goes by a second product: two bf16 parts hold 16 bits of
+  // it. (relu of a bf16 or 8-bit value needs one.) A bf16 dW takes the rounded value
+  // alone, which is what a bf16 forward product read.
+  // 8191 rows 14336 -> 4096, silu from e4m3, against the formula in 64 bits: fp32 dW
+  // 1.5e-3 off with one product, 2.1e-6 with two (946 and 1921 us);
+  // bf16 dW 2.25e-3 with one, and 1.66e-3 is its own rounding alone.
+  if (x_act > MAO_ACT_RELU && dY.dtype == MAO_BF16 && dW.dtype == MAO_F32) {
+    MAO_TRY(rebuild(true));
+    p.e.add = dW.data;
+    p.e.ldadd = dW.ld;
+    p.e.add_dtype = dW.dtype;
+    MAO_TRY(launch_linear(dY.dtype, p, w.part, nullptr, s));
+  }
   if (dbias)
     MAO_TRY(launch_partial_sum(w.sums, p.M, lin_sum_rows(dY.dtype, p.M, p.N, p.K), p.M, dbias,
                                nullptr, 0, accumulate != 0, s));

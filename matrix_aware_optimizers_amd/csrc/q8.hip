@@ -82,10 +82,19 @@ __global__ __launch_bounds__(256) void q8_quantize_kernel(const T* x, int64_t ld
   }
 }
 
+// v[i] <- v[i] - bf16(v[i]), exact in fp32; 0 where bf16(v[i]) is not finite
+__device__ __forceinline__ void rest8(float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float h = bf16_to_f32(f32_to_bf16(v[i]));
+    v[i] = fabsf(h) < INFINITY ? v[i] - h : 0.f;
+  }
+}
+
 template <int FMT>
 __global__ __launch_bounds__(256) void q8_dequantize_kernel(Q8View q, int rows, int cols, int act,
-                                                            void* y, int dtype, int64_t ldy,
-                                                            int nch) {
+                                                            int rest, void* y, int dtype,
+                                                            int64_t ldy, int nch) {
   const int64_t total = (int64_t)rows * nch;
   for (int64_t base = (int64_t)blockIdx.x * 256; base < total; base += (int64_t)gridDim.x * 256) {
     const int64_t br = base / nch;
@@ -101,16 +110,20 @@ __global__ __launch_bounds__(256) void q8_dequantize_kernel(Q8View q, int rows, 
     q8_decode4<FMT>(c.w, sc, hi + 4);
     act_apply(act, lo);
     act_apply(act, hi);
+    if (rest) {
+      rest8(lo);
+      rest8(hi);
+    }
     const int64_t off = (int64_t)it.row * ldy + col;
     store8n_any(y, dtype, off, lo, valid);
     if (valid > 8) store8n_any(y, dtype, off + 8, hi, valid - 8);
   }
 }
 
-// y = act(x): 8 columns per thread
+// y = act(x), or its rest: 8 columns per thread
 template <typename T>
 __global__ __launch_bounds__(256) void act_kernel(const T* x, int64_t ldx, int rows, int cols,
-                                                  int act, T* y, int64_t ldy, int nch) {
+                                                  int act, int rest, T* y, int64_t ldy, int nch) {
   const int64_t total = (int64_t)rows * nch;
   for (int64_t base = (int64_t)blockIdx.x * 256; base < total; base += (int64_t)gridDim.x * 256) {
     const int64_t br = base / nch;
@@ -121,6 +134,7 @@ __global__ __launch_bounds__(256) void act_kernel(const T* x, int64_t ldx, int r
     float v[8];
     r.get(v);
     act_apply(act, v);
+    if (rest) rest8(v);
     store8n_any(y, sizeof(T) == 2 ? MAO_BF16 : MAO_F32, (int64_t)it.row * ldy + it.c * 8, v,
                 cols - it.c * 8);
   }
@@ -149,30 +163,30 @@ mao_status launch_q8_quantize(const void* x, int dtype, int64_t ldx, int rows, i
   return MAO_OK;
 }
 
-mao_status launch_act(const void* x, int dtype, int64_t ldx, int rows, int cols, int act, void* y,
-                      int64_t ldy, hipStream_t s) {
+mao_status launch_act(const void* x, int dtype, int64_t ldx, int rows, int cols, int act, bool rest,
+                      void* y, int64_t ldy, hipStream_t s) {
   const int nch = (int)ceil_div(cols, 8);
   const dim3 grid(q8_grid((int64_t)rows * nch));
   if (dtype == MAO_BF16)
     hipLaunchKernelGGL((act_kernel<bf16_t>), grid, dim3(256), 0, s, (const bf16_t*)x, ldx, rows,
-                       cols, act, (bf16_t*)y, ldy, nch);
+                       cols, act, (int)rest, (bf16_t*)y, ldy, nch);
   else
     hipLaunchKernelGGL((act_kernel<float>), grid, dim3(256), 0, s, (const float*)x, ldx, rows, cols,
-                       act, (float*)y, ldy, nch);
+                       act, (int)rest, (float*)y, ldy, nch);
   MAO_LAUNCH_CHECK();
   return MAO_OK;
 }
 
-mao_status launch_q8_dequantize(Q8View q, int fmt, int rows, int cols, int act, void* y, int dtype,
-                                int64_t ldy, hipStream_t s) {
+mao_status launch_q8_dequantize(Q8View q, int fmt, int rows, int cols, int act, bool rest, void* y,
+                                int dtype, int64_t ldy, hipStream_t s) {
   const int nch = (int)ceil_div(cols, 16);
   const dim3 grid(q8_grid((int64_t)rows * nch));
   if (fmt == MAO_Q8_INT8)
     hipLaunchKernelGGL((q8_dequantize_kernel<MAO_Q8_INT8>), grid, dim3(256), 0, s, q, rows, cols,
-                       act, y, dtype, ldy, nch);
+                       act, (int)rest, y, dtype, ldy, nch);
   else
     hipLaunchKernelGGL((q8_dequantize_kernel<MAO_Q8_E4M3>), grid, dim3(256), 0, s, q, rows, cols,
-                       act, y, dtype, ldy, nch);
+                       act, (int)rest, y, dtype, ldy, nch);
   MAO_LAUNCH_CHECK();
   return MAO_OK;
 }
