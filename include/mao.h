@@ -414,8 +414,9 @@ MAO_API mao_status adamw_step(void* w, int32_t w_dtype, const void* g, int32_t g
  * The conventions above hold (row-major views, ld a multiple of 8, caller-owned
  * buffers, host-side validation, no synchronisation, bitwise repeatable).
  * Vectors (gamma, beta, bias) are contiguous and 16-byte aligned, fp32 or bf16;
- * statistics and vector gradients are fp32. Storage between cols and the next
- * multiple of 8 of a row may be read and is never written. Arithmetic and sums
+ * statistics and vector gradients are fp32. Of the storage past a row's last
+ * element, only the rest of that element's 16-byte piece may be read (of a
+ * checkpoint's codes too), and none is written. Arithmetic and sums
  * are fp32; each result is rounded once, as it is stored. Sizes are at least 1
  * (MAO_E_SHAPE) and at most 2^20.
  */

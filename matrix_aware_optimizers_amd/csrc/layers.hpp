@@ -7,11 +7,14 @@
 
 namespace mao {
 
-// Eight consecutive elements (16-byte aligned) as fp32.
+// Eight consecutive elements (16-byte aligned) as fp32. load_cut reads, of a run with
+// `valid` elements of a row, only the 16-byte pieces that hold one (the first one
+// twice): storage may end with the row, and a piece never crosses a page.
 template <typename T> struct Raw8;
 template <> struct Raw8<bf16_t> {
   uint4 a;
   __device__ __forceinline__ void load(const bf16_t* p) { a = *(const uint4*)p; }
+  __device__ __forceinline__ void load_cut(const bf16_t* p, int /*valid*/) { load(p); }
   __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
   // the compiler may not carry values derived from here on across this point
   __device__ __forceinline__ void opaque() {
@@ -32,6 +35,10 @@ template <> struct Raw8<float> {
     a = *(const float4*)p;
     b = *(const float4*)(p + 4);
   }
+  __device__ __forceinline__ void load_cut(const float* p, int valid) {
+    a = *(const float4*)p;
+    b = *(const float4*)(p + (valid > 4 ? 4 : 0));
+  }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void opaque() {
     asm volatile("" : "+v"(a.x), "+v"(a.y), "+v"(a.z), "+v"(a.w));
@@ -43,14 +50,15 @@ template <> struct Raw8<float> {
   }
 };
 
-__device__ __forceinline__ void load8_any(const void* p, int dtype, int64_t off, float (&v)[8]) {
+__device__ __forceinline__ void load8_any(const void* p, int dtype, int64_t off, float (&v)[8],
+                                          int valid) {
   if (dtype == MAO_BF16) {
     Raw8<bf16_t> r;
     r.load((const bf16_t*)p + off);
     r.get(v);
   } else {
     Raw8<float> r;
-    r.load((const float*)p + off);
+    r.load_cut((const float*)p + off, valid);
     r.get(v);
   }
 }

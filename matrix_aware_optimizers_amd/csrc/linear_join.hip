@@ -32,7 +32,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinProblem P, const fl
       float z[8];
       const int64_t off = (int64_t)row * e.ldzi + col;
       if (e.z_kind <= MAO_BF16) {
-        load8_any(e.z_in, e.z_kind, off, z);
+        load8_any(e.z_in, e.z_kind, off, z, valid);
       } else {
         const uint2 q = *(const uint2*)((const uint8_t*)e.z_in + off);
         const float sc = q8_scale_value(e.z_scales[(int64_t)row * e.ldzs + (col >> 5)]);
@@ -46,7 +46,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinProblem P, const fl
     if (e.bias != nullptr) {
       float b[8];
       if (valid >= 8) {
-        load8_any(e.bias, e.bias_dtype, col, b);
+        load8_any(e.bias, e.bias_dtype, col, b, 8);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) b[i] = i < valid ? load1_any(e.bias, e.bias_dtype, col + i) : 0.f;
@@ -59,7 +59,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinProblem P, const fl
   }
   if (e.add != nullptr) {
     float a[8];
-    load8_any(e.add, e.add_dtype, (int64_t)row * e.ldadd + col, a);
+    load8_any(e.add, e.add_dtype, (int64_t)row * e.ldadd + col, a, valid);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += a[i];
   }

@@ -136,15 +136,16 @@ __device__ __forceinline__ void put8(void* p, int dtype, int64_t off, const floa
   }
 }
 
-// Eight values of a tensor, as loaded (BF: known to be bf16).
+// Eight values of a tensor, as loaded (BF: known to be bf16); of fewer valid ones the
+// 16-byte pieces that hold one (as Raw8::load_cut).
 template <bool BF> struct RawT {
   uint4 a, b[1];
-  __device__ __forceinline__ void load(const void* p, int dtype, int64_t off) {
+  __device__ __forceinline__ void load(const void* p, int dtype, int64_t off, int valid) {
     if (BF || dtype == MAO_BF16) {
       a = *(const uint4*)((const bf16_t*)p + off);
     } else {
       a = *(const uint4*)((const float*)p + off);
-      b[0] = *(const uint4*)((const float*)p + off + 4);
+      b[0] = *(const uint4*)((const float*)p + off + (valid > 4 ? 4 : 0));
     }
   }
   __device__ __forceinline__ void get(int dtype, float (&v)[8]) const {
@@ -192,10 +193,11 @@ __device__ __forceinline__ void finish(const f32x16_t* acc, float* reg, const Li
         t.z.a.y = w.y;
         t.scale = e.z_scales[(int64_t)row * e.ldzs + (col >> 5)];
       } else {
-        t.z.load(e.z_in, e.z_kind, off);
+        t.z.load(e.z_in, e.z_kind, off, P.N - col);
       }
     }
-    if (e.add != nullptr) t.a.load(e.add, e.add_dtype, (int64_t)row * e.ldadd + col);
+    if (e.add != nullptr)
+      t.a.load(e.add, e.add_dtype, (int64_t)row * e.ldadd + col, P.N - col);
   };
   Inputs t0, t1;
   load(0, t0);

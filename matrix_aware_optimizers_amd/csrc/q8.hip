@@ -45,8 +45,8 @@ __global__ __launch_bounds__(256) void q8_quantize_kernel(const T* x, int64_t ld
       float lo[8], hi[8];
       Raw8<T> r0, r1;
       const T* p = x + (int64_t)it.row * ldx + col;
-      if (valid > 0) r0.load(p); else r0.zero();
-      if (valid > 8) r1.load(p + 8); else r1.zero();
+      if (valid > 0) r0.load_cut(p, valid); else r0.zero();
+      if (valid > 8) r1.load_cut(p + 8, valid - 8); else r1.zero();
       r0.get(lo);
       r1.get(hi);
 #pragma unroll
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(256) void act_kernel(const T* x, int64_t ldx, int r
     const Item it = item_of(br, (int)(base - br * nch), nch);
     if (it.row >= rows) continue;
     Raw8<T> r;
-    r.load(x + (int64_t)it.row * ldx + it.c * 8);
+    r.load_cut(x + (int64_t)it.row * ldx + it.c * 8, cols - it.c * 8);
     float v[8];
     r.get(v);
     act_apply(act, v);
