@@ -58,8 +58,18 @@ mao_mat view(const at::Tensor& t, int64_t dev) {
                  dtype_code(t)};
 }
 
+// A checkpoint's two tensors are attributes that a program may have set itself: all that
+// the class checks as it is made is checked here again.
 mao_q8 checkpoint(const at::Tensor& codes, const at::Tensor& scales, int64_t dev) {
-  if (codes.dim() != 2 || scales.dim() != 2) fail(PyExc_ValueError, "a checkpoint is 2-D");
+  if (codes.scalar_type() != at::kChar && codes.scalar_type() != at::kFloat8_e4m3fn)
+    fail(PyExc_TypeError, "a checkpoint's codes must be int8 or float8_e4m3fn");
+  if (scales.scalar_type() != at::kByte)
+    fail(PyExc_TypeError, "a checkpoint's scales must be uint8");
+  if (codes.dim() != 2 || scales.dim() != 2 || (codes.stride(1) != 1 && codes.size(1) != 1) ||
+      (scales.stride(1) != 1 && scales.size(1) != 1))
+    fail(PyExc_ValueError, "a checkpoint's codes and scales must be 2-D and row-major");
+  if (scales.size(0) != codes.size(0) || scales.size(1) < (codes.size(1) + 31) / 32)
+    fail(PyExc_ValueError, "a checkpoint's scales need one byte per row and 32 columns");
   on_device(codes, dev);
   on_device(scales, dev);
   return mao_q8{codes.data_ptr(), (uint8_t*)scales.data_ptr(), codes.size(0), codes.size(1),

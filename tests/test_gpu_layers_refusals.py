@@ -1,0 +1,64 @@
+"""What the layer calls refuse before anything is launched (GPU)."""
+import pytest
+
+from tests.helpers import log
+
+pytestmark = pytest.mark.gpu
+
+
+def _checkpoint(lib):
+    import torch
+    x = torch.randn((8, 72), device="cuda")
+    return x, lib.q8_quantize(x)
+
+
+def test_checkpoint_whose_parts_were_replaced(gpu_lib):
+    """codes and scales are plain attributes: what Q8 refuses as it is made is also
+    refused where it is used."""
+    import torch
+    log("replaced codes and scales")
+    lib = gpu_lib
+    x, _ = _checkpoint(lib)
+    mean = torch.zeros(8, device="cuda")
+    w = torch.randn((16, 72), device="cuda")
+    dy = torch.randn((8, 16), device="cuda")
+
+    def uses(q):
+        yield lambda: lib.q8_dequantize(q)
+        yield lambda: lib.q8_quantize(x, out=q)
+        yield lambda: lib.layer_norm_backward(x, q, None, mean, mean)
+        yield lambda: lib.linear_backward_input(dy, w, act="relu", preact=q)
+        yield lambda: lib.linear_backward_weight(dy, q)
+
+    def replaced(**parts):
+        q = _checkpoint(lib)[1]
+        for k, v in parts.items():
+            setattr(q, k, v)
+        return q
+
+    _, q = _checkpoint(lib)
+    wide = torch.zeros((8, 256), dtype=torch.int8, device="cuda")
+    for bad, error in ((replaced(scales=q.scales[:3]), ValueError),
+                       (replaced(scales=q.scales[:, :2]), ValueError),
+                       (replaced(scales=q.scales[0]), ValueError),
+                       (replaced(scales=torch.zeros((8, 8), dtype=torch.uint8, device="cuda")[:, ::2]),
+                        ValueError),
+                       (replaced(scales=q.scales.to(torch.int8)), TypeError),
+                       (replaced(codes=wide[:, ::3][:, :72]), ValueError),
+                       (replaced(codes=q.codes.float()), TypeError),
+                       (replaced(codes=q.codes.view(torch.uint8)), TypeError),
+                       (replaced(scales=q.scales.cpu()), ValueError)):
+        for use in uses(bad):
+            with pytest.raises(error):
+                use()
+
+
+def test_quantise_into_something_else(gpu_lib):
+    import types
+
+    import torch
+    log("quantise into something else")
+    x, q = _checkpoint(gpu_lib)
+    with pytest.raises(TypeError):
+        gpu_lib.q8_quantize(x, out=types.SimpleNamespace(codes=torch.zeros((8, 96), device="cuda")[:, :72],
+                                                         scales=q.scales))
