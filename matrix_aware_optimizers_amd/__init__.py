@@ -555,6 +555,18 @@ def _act(act):
     return int(act)
 
 
+def _result_type(dtype, default):
+    """The code of a result's dtype."""
+    if dtype is None:
+        return default
+    torch = _torch()
+    if dtype == torch.float32:
+        return F32
+    if dtype == torch.bfloat16:
+        return BF16
+    raise TypeError(f"unsupported result dtype {dtype}: float32 or bfloat16 is needed")
+
+
 def q8_quantize(X, fmt="int8", out=None) -> Q8:
     """Keeps X (bf16 or fp32) in 8 bits."""
     if out is not None:
@@ -567,8 +579,7 @@ def q8_quantize(X, fmt="int8", out=None) -> Q8:
 
 def q8_dequantize(q: Q8, act="none", dtype=None, out=None):
     """act(q) as a tensor (bf16 unless ``dtype`` or ``out`` says fp32)."""
-    return _run("q8_dequantize", q, _act(act),
-                F32 if dtype is not None and dtype == _torch().float32 else BF16, out)
+    return _run("q8_dequantize", q, _act(act), _result_type(dtype, BF16), out)
 
 
 def layer_norm(X, gamma=None, beta=None, *, eps=1e-5, out=None, stats=True):
@@ -605,8 +616,7 @@ def linear_backward_weight(dY, X, *, x_act="none", dtype=None, out=None, dbias=N
     given."""
     if accumulate and (out is None or dbias is None):
         raise ValueError("accumulate needs out and dbias")
-    return _run("linear_backward_weight", dY, X, _act(x_act),
-                BF16 if dtype is not None and dtype == _torch().bfloat16 else F32, out, dbias,
+    return _run("linear_backward_weight", dY, X, _act(x_act), _result_type(dtype, F32), out, dbias,
                 bool(accumulate))
 
 
