@@ -454,7 +454,9 @@ def adamw_step(w, g, m, v, t: int, *, lr, beta1=0.9, beta2=0.95, eps=1e-8, weigh
 #
 # Matrices are 2-D tensors that meet the layout rule (``padded`` copies one that
 # does not, ``empty_matrix`` makes one). All work runs on the current stream of
-# the tensors' device. Results that are not passed in are allocated here.
+# the tensors' device. Results that are not passed in are allocated here. The calls
+# record no autograd graph (their backward passes are calls of their own): a tensor
+# that requires a gradient is refused unless gradients are off (torch.no_grad).
 
 class Q8:
     """8-bit checkpoint of a 2-D tensor: ``codes`` (int8 or float8_e4m3fn, row

@@ -11,6 +11,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -42,6 +43,15 @@ void on_device(const at::Tensor& t, int64_t dev) {
   if (t.get_device() != dev) fail(PyExc_ValueError, "tensors on different devices");
 }
 
+// The calls have their own backward calls and record no graph: a tensor whose gradient
+// autograd is to find would lose it without a word.
+void no_graph(const at::Tensor& t) {
+  if (t.requires_grad() && c10::GradMode::is_enabled())
+    fail(PyExc_RuntimeError,
+         "the layer operators record no autograd graph, and a tensor requires a gradient: call "
+         "them under torch.no_grad(), with their own backward calls, or detach the tensor");
+}
+
 int32_t dtype_code(const at::Tensor& t) {
   if (t.scalar_type() == at::kFloat) return MAO_F32;
   if (t.scalar_type() == at::kBFloat16) return MAO_BF16;
@@ -52,6 +62,7 @@ mao_mat view(const at::Tensor& t, int64_t dev) {
   if (t.dim() != 2 || (t.stride(1) != 1 && t.size(1) != 1))
     fail(PyExc_ValueError, "expected a 2-D row-major tensor (unit column stride)");
   on_device(t, dev);
+  no_graph(t);
   const int64_t rows = t.size(0), cols = t.size(1);
   // the row stride of a single row means nothing
   return mao_mat{t.data_ptr(), rows, cols, rows == 1 ? (cols + 7) & ~int64_t(7) : t.stride(0),
@@ -137,6 +148,7 @@ struct Vec {
       throw Raised{};
     }
     on_device(t, dev);
+    no_graph(t);
     dtype = dtype_code(t);
     if (floats && dtype != MAO_F32) {
       PyErr_Format(PyExc_TypeError, "%s must be float32", name);

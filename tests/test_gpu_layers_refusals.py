@@ -62,3 +62,37 @@ def test_quantise_into_something_else(gpu_lib):
     with pytest.raises(TypeError):
         gpu_lib.q8_quantize(x, out=types.SimpleNamespace(codes=torch.zeros((8, 96), device="cuda")[:, :72],
                                                          scales=q.scales))
+
+
+def test_tensors_that_autograd_follows(gpu_lib):
+    """The calls record no graph: with gradients on, a tensor that requires one is
+    refused rather than cut off; with gradients off it is an ordinary tensor."""
+    import torch
+    log("requires_grad")
+    lib = gpu_lib
+    x, w, b = (torch.randn(s, device="cuda") for s in ((8, 72), (16, 72), (16,)))
+    dy, z, g = (torch.randn(s, device="cuda") for s in ((8, 16), (8, 72), (72,)))
+    _, mean, rstd = lib.layer_norm(x, g)
+    q = lib.q8_quantize(x)
+    r = lambda t: t.clone().requires_grad_(True)
+    calls = [(lib.linear, (x, w, b), {}), (lib.layer_norm, (x, g, g), {}),
+             (lib.q8_quantize, (x,), {}), (lib.layer_norm_backward, (x, z, g, mean, rstd), {}),
+             (lib.layer_norm_backward, (x, q, g, mean, rstd), {}),
+             (lib.linear_backward_input, (dy, w), {"act": "silu", "preact": z}),
+             (lib.linear_backward_weight, (dy, x), {})]
+    for fn, args, kw in calls:
+        for i, a in enumerate(args):
+            if a is q:
+                continue
+            some = [*args[:i], torch.nn.Parameter(a) if i % 2 else r(a), *args[i + 1:]]
+            with pytest.raises(RuntimeError, match="no_grad"):
+                fn(*some, **kw)
+            with torch.no_grad():
+                fn(*some, **kw)
+            with torch.inference_mode():
+                fn(*some, **kw)
+        fn(*args, **kw)
+    with pytest.raises(RuntimeError, match="no_grad"):
+        lib.linear_backward_input(dy, w, act="silu", preact=r(z))
+    with pytest.raises(RuntimeError, match="no_grad"):
+        lib.linear(x, w, residual=r(dy))
