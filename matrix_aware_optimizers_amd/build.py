@@ -4,7 +4,8 @@ Usage: ``python -m matrix_aware_optimizers_amd.build`` (or call ``build()``).
 Every ``.hip`` file under ``csrc/`` is compiled to an object with hipcc for
 gfx950 and the objects are linked into ``libmao.so``. Objects go to
 ``_build/`` at the repository root. ``csrc/binding.cpp`` (host code: torch
-tensors to the C ABI, for the layer operators) becomes ``_layers.so`` beside it.
+tensors to the C ABI, for the layer operators) becomes ``_layers.so`` beside it,
+where g++, torch's headers and Python's are there; the library needs hipcc alone.
 """
 from __future__ import annotations
 
@@ -51,8 +52,24 @@ def _run(cmd, what):
         raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
 
 
+def _binding_lacks():
+    """What csrc/binding.cpp needs and this machine does not have, or None."""
+    if shutil.which("g++") is None:
+        return "g++"
+    try:
+        import torch
+    except ImportError:
+        return "torch"
+    inc = os.path.join(os.path.dirname(torch.__file__), "include", "ATen", "core", "Tensor.h")
+    if not os.path.exists(inc):
+        return "torch's headers"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python's headers"
+    return None
+
+
 def _compile_binding() -> str:
-    """The object of csrc/binding.cpp (needs the headers of torch and Python)."""
+    """The object of csrc/binding.cpp."""
     import torch
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     obj = os.path.join(OBJ, "binding.o")
@@ -73,22 +90,29 @@ def _link_binding(obj: str):
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source for gfx950 and link libmao.so (and _layers.so);
-    returns its path."""
+    """Compile every HIP source for gfx950 and link libmao.so; returns its path. Then
+    the binding of the layer calls, _layers.so: left out, and said so, where its
+    compiler or headers are missing; an error in it is raised with the library built."""
     if not os.path.exists(HIPCC):
         raise RuntimeError(f"hipcc not found at {HIPCC}")
     os.makedirs(OBJ, exist_ok=True)
     srcs = sources()
     workers = min(len(srcs), max(1, (os.cpu_count() or 2) // 2))
+    lacks = _binding_lacks()
     with cf.ThreadPoolExecutor(max_workers=workers) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = None if lacks else ex.submit(_compile_binding)
         objs = list(ex.map(_compile, srcs))
-        binding = binding.result()
     tmp = LIB + ".tmp"
     _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Wl,-soname,libmao.so", "-o", tmp,
           *objs], "link of libmao.so")
     shutil.move(tmp, LIB)
-    _link_binding(binding)
+    if os.path.exists(BINDING):  # of the library before
+        os.remove(BINDING)
+    if lacks:
+        print(f"built {LIB} without _layers.so (the Python layer calls): no {lacks}",
+              file=sys.stderr)
+        return LIB
+    _link_binding(binding.result())
     if verbose:
         print(f"built {LIB}")
     return LIB
