@@ -491,7 +491,8 @@ MAO_API mao_status mao_layer_norm_backward(mao_mat dY, const mao_mat* X, const m
 MAO_API size_t mao_linear_workspace_size(int64_t rows, int64_t k, int64_t n, int32_t dtype);
 MAO_API size_t mao_linear_backward_input_workspace_size(int64_t rows, int64_t k, int64_t n,
                                                         int32_t dtype);
-/* rebuilt != 0: the input comes from a checkpoint or through x_act. */
+/* rebuilt != 0: the input comes from a checkpoint or through x_act. With dbias NULL a
+ * call may need less. */
 MAO_API size_t mao_linear_backward_weight_workspace_size(int64_t rows, int64_t k, int64_t n,
                                                          int32_t dtype, int32_t rebuilt);
 

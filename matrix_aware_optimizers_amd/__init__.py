@@ -592,7 +592,8 @@ def layer_norm(X, gamma=None, beta=None, *, eps=1e-5, out=None, stats=True):
 
 def layer_norm_backward(dY, X, gamma, mean, rstd, *, add=None, out=None, dgamma=None, dbeta=None):
     """(dX, dgamma, dbeta) of layer_norm. X: its input, or the input's Q8
-    checkpoint. ``add`` joins dX (the skip connection's gradient)."""
+    checkpoint. ``add`` joins dX (the skip connection's gradient). ``dgamma``,
+    ``dbeta``: the vector to write, or False if it is not wanted (None comes back)."""
     return _run("layer_norm_backward", dY, X, gamma, mean, rstd, add, out, dgamma, dbeta)
 
 
@@ -615,7 +616,8 @@ def linear_backward_weight(dY, X, *, x_act="none", dtype=None, out=None, dbias=N
     a recomputed activation costs an fp32 dW a second product (it holds 16 bits of
     the activation; a bf16 dW takes it rounded to bf16). With
     ``accumulate`` both are added to ``out`` and ``dbias``, which then have to be
-    given."""
+    given. ``dbias``: the vector to write, or False for a layer without a bias (None
+    comes back)."""
     if accumulate and (out is None or dbias is None):
         raise ValueError("accumulate needs out and dbias")
     return _run("linear_backward_weight", dY, X, _act(x_act), _result_type(dtype, F32), out, dbias,

@@ -167,9 +167,30 @@ at::Tensor result(PyObject* o, int64_t rows, int64_t cols, at::ScalarType type,
   return ld == cols ? t : t.narrow(1, 0, cols);
 }
 
-at::Tensor vector_result(PyObject* o, int64_t n, const at::Tensor& like) {
-  return o != Py_None ? tensor(o) : at::empty({n}, like.options().dtype(at::kFloat));
+PyObject* wrap(const at::Tensor& t, PyObject* given) {
+  if (given != Py_None) {
+    Py_INCREF(given);
+    return given;
+  }
+  return THPVariable_Wrap(t);
 }
+
+// A vector gradient: passed in, new (None) or not wanted (False).
+struct VecResult {
+  PyObject* given;
+  at::Tensor t;
+  float* p = nullptr;
+  VecResult(PyObject* o, int64_t n, int64_t dev, const char* name, const at::Tensor& like)
+      : given(o) {
+    if (o == Py_False) return;
+    if (o == Py_None)
+      t = at::empty({n}, like.options().dtype(at::kFloat));
+    else
+      t = (Vec(o, n, dev, name, true), tensor(o));
+    p = (float*)t.data_ptr();
+  }
+  PyObject* object() const { return given == Py_False ? Py_NewRef(Py_None) : wrap(t, given); }
+};
 
 struct Workspace {
   PyObject* keep = nullptr;
@@ -205,14 +226,6 @@ int64_t integer(PyObject* o) {
 }
 
 at::ScalarType type_of(int64_t code) { return code == MAO_BF16 ? at::kBFloat16 : at::kFloat; }
-
-PyObject* wrap(const at::Tensor& t, PyObject* given) {
-  if (given != Py_None) {
-    Py_INCREF(given);
-    return given;
-  }
-  return THPVariable_Wrap(t);
-}
 
 template <typename F>
 PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
@@ -310,7 +323,7 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // (dY, X, gamma, mean, rstd, add, out, dgamma, dbeta, device, stream)
-// -> (dX, dgamma, dbeta)
+// -> (dX, dgamma, dbeta); dgamma or dbeta False: not computed, None
 PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 11, [&]() -> PyObject* {
     const int64_t dev = integer(a[9]), stream = integer(a[10]);
@@ -321,17 +334,17 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Vec mean(a[3], dy.rows, dev, "mean", true), rstd(a[4], dy.rows, dev, "rstd", true);
     if (!mean.p || !rstd.p) fail(PyExc_ValueError, "mean and rstd of the forward pass are needed");
     const Opt add(a[5], dev);
-    const Vec gg(a[7], dy.cols, dev, "dgamma", true), gb(a[8], dy.cols, dev, "dbeta", true);
+    const VecResult dgamma(a[7], dy.cols, dev, "dgamma", DY), dbeta(a[8], dy.cols, dev, "dbeta", DY);
     const at::Tensor out = result(a[6], dy.rows, dy.cols, DY.scalar_type(), DY);
-    const at::Tensor dgamma = vector_result(a[7], dy.cols, DY);
-    const at::Tensor dbeta = vector_result(a[8], dy.cols, DY);
-    const Workspace ws(mao_layer_norm_backward_workspace_size(dy.rows, dy.cols), dev, stream);
+    const Workspace ws(dgamma.p || dbeta.p
+                           ? mao_layer_norm_backward_workspace_size(dy.rows, dy.cols)
+                           : 0,
+                       dev, stream);
     check(mao_layer_norm_backward(dy, x.mat, x.q8, g.p, g.dtype, (const float*)mean.p,
                                   (const float*)rstd.p, add.p, view(out, dev),
-                                  (float*)dgamma.data_ptr(), (float*)dbeta.data_ptr(), ws.p,
-                                  ws.bytes, (void*)stream),
+                                  dgamma.p, dbeta.p, ws.p, ws.bytes, (void*)stream),
           "mao_layer_norm_backward");
-    return Py_BuildValue("NNN", wrap(out, a[6]), wrap(dgamma, a[7]), wrap(dbeta, a[8]));
+    return Py_BuildValue("NNN", wrap(out, a[6]), dgamma.object(), dbeta.object());
   });
 }
 
@@ -370,24 +383,23 @@ PyObject* linear_backward_input(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (dY, X, x_act, result type, out, dbias, accumulate, device, stream) -> (dW, dbias)
+// (dY, X, x_act, result type, out, dbias, accumulate, device, stream) -> (dW, dbias); dbias
+// False: not computed, None
 PyObject* linear_backward_weight(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 9, [&]() -> PyObject* {
     const int64_t dev = integer(a[7]), stream = integer(a[8]), act = integer(a[2]);
     const at::Tensor& DY = tensor(a[0]);
     const mao_mat dy = view(DY, dev);
     const Kept x(a[1], dev);
-    const Vec gb(a[5], dy.cols, dev, "dbias", true);
+    const VecResult dbias(a[5], dy.cols, dev, "dbias", DY);
     const at::Tensor out = result(a[4], dy.cols, x.cols, type_of(integer(a[3])), DY);
-    const at::Tensor dbias = vector_result(a[5], dy.cols, DY);
     const Workspace ws(mao_linear_backward_weight_workspace_size(
                            dy.rows, x.cols, dy.cols, dy.dtype, x.q8 != nullptr || act != 0),
                        dev, stream);
-    check(mao_linear_backward_weight(dy, x.mat, x.q8, (int32_t)act, view(out, dev),
-                                     (float*)dbias.data_ptr(), a[6] == Py_True, ws.p, ws.bytes,
-                                     (void*)stream),
+    check(mao_linear_backward_weight(dy, x.mat, x.q8, (int32_t)act, view(out, dev), dbias.p,
+                                     a[6] == Py_True, ws.p, ws.bytes, (void*)stream),
           "mao_linear_backward_weight");
-    return Py_BuildValue("NN", wrap(out, a[4]), wrap(dbias, a[5]));
+    return Py_BuildValue("NN", wrap(out, a[4]), dbias.object());
   });
 }
 

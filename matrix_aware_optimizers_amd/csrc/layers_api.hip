@@ -96,7 +96,7 @@ struct WeightWs {
   char *x, *part;
   float* sums;
   int64_t ldx;
-  size_t bytes;
+  size_t bytes, bare;  // bare: without a bias gradient
 };
 WeightWs carve_weight(void* base, int64_t rows, int64_t k, int64_t n, int dtype, bool rebuilt) {
   Carver c(base);
@@ -104,6 +104,7 @@ WeightWs carve_weight(void* base, int64_t rows, int64_t k, int64_t n, int dtype,
   w.ldx = ws_ld(k);
   if (rebuilt) w.x = c.take<char>((size_t)rows * w.ldx * dtype_size(dtype));
   w.part = c.take<char>(lin_workspace(dtype, n, k, rows));
+  w.bare = c.used;
   w.sums = c.take<float>((size_t)lin_sum_rows(dtype, n, k, rows) * n);
   w.bytes = c.used;
   return w;
@@ -391,11 +392,12 @@ mao_status mao_linear_backward_weight(mao_mat dY, const mao_mat* X, const mao_q8
   MAO_TRY(check_floats("dbias", dbias));
   const bool rebuilt = X8 != nullptr || x_act != MAO_ACT_NONE;
   const WeightWs w = carve_weight(workspace, dY.rows, dW.cols, dW.rows, dY.dtype, rebuilt);
-  MAO_TRY(check_workspace(workspace, workspace_bytes, w.bytes));
+  const size_t need = dbias ? w.bytes : w.bare;
+  MAO_TRY(check_workspace(workspace, workspace_bytes, need));
   Buffers b;
   b.out(range_of(dW));
   if (dbias) b.out(range_of(dbias, dW.rows * 4));
-  b.out(range_of(workspace, (int64_t)w.bytes));
+  if (need) b.out(range_of(workspace, (int64_t)need));
   b.in(range_of(dY));
   if (X) b.in(range_of(*X));
   b.in(X8);

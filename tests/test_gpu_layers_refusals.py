@@ -96,3 +96,48 @@ def test_tensors_that_autograd_follows(gpu_lib):
         lib.linear_backward_input(dy, w, act="silu", preact=r(z))
     with pytest.raises(RuntimeError, match="no_grad"):
         lib.linear(x, w, residual=r(dy))
+
+
+def test_vector_gradients_that_are_not_wanted(gpu_lib):
+    """False leaves a vector gradient out: the rest comes out bit for bit the same, and
+    the C entry point asks for no workspace for it."""
+    import ctypes
+
+    import torch
+    log("unwanted vector gradients")
+    lib = gpu_lib
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    x, dy = (torch.randn((300, 72), generator=gen, device="cuda") for _ in range(2))
+    gamma = torch.rand(72, generator=gen, device="cuda")
+    _, mean, rstd = lib.layer_norm(x, gamma)
+    dx, dg, db = lib.layer_norm_backward(dy, x, gamma, mean, rstd)
+    for wg, wb in ((False, None), (None, False), (False, False)):
+        got = lib.layer_norm_backward(dy, x, gamma, mean, rstd, dgamma=wg, dbeta=wb)
+        assert torch.equal(got[0], dx)
+        assert got[1] is None if wg is False else torch.equal(got[1], dg)
+        assert got[2] is None if wb is False else torch.equal(got[2], db)
+    for rows, n in ((300, 72), (5000, 40)):  # the second with K split
+        x = torch.randn((rows, 56), generator=gen, device="cuda").bfloat16()
+        dy = torch.randn((rows, n), generator=gen, device="cuda").bfloat16()
+        for act in ("none", "gelu"):
+            dw, db = lib.linear_backward_weight(dy, x, x_act=act)
+            got, none = lib.linear_backward_weight(dy, x, x_act=act, dbias=False)
+            assert none is None and torch.equal(got, dw)
+            twice, none = lib.linear_backward_weight(dy, x, x_act=act, out=got, dbias=False,
+                                                     accumulate=True)
+            full = dw.clone()
+            lib.linear_backward_weight(dy, x, x_act=act, out=full, dbias=db, accumulate=True)
+            assert none is None and torch.equal(twice, full)
+    # 8 rows: one part, nothing rebuilt; without dbias no workspace at all
+    x, dy = (torch.randn((8, 72), generator=gen, device="cuda") for _ in range(2))
+    want, _ = lib.linear_backward_weight(dy, x)
+    out = torch.empty_like(want)
+    c = lib.load()
+    call = lambda db: c.mao_linear_backward_weight(
+        lib.mat(dy), ctypes.byref(lib.mat(x)), None, 0, lib.mat(out), db, 0, None, 0,
+        torch.cuda.current_stream().cuda_stream)
+    assert c.mao_linear_backward_weight_workspace_size(8, 72, 72, lib.F32, 0) > 0
+    assert call(torch.empty(72, device="cuda").data_ptr()) == 7  # MAO_E_WORKSPACE
+    assert call(None) == 0
+    assert torch.equal(out, want)
