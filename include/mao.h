@@ -535,6 +535,14 @@ MAO_API mao_status mao_linear_backward_weight(mao_mat dY, const mao_mat* X, cons
                                               int32_t accumulate, void* workspace,
                                               size_t workspace_bytes, void* stream);
 
+/* Test hook: the tile shape and the K split that a linear product of these sizes is cut
+ * into. product: 0 forward, 1 input gradient, 2 weight gradient; mixed != 0: a bf16
+ * product (not a weight gradient) with an fp32 result or joining tensor. Up to 16 rows
+ * the forward product is not cut (tile 16 x 16, split 1). */
+MAO_API mao_status mao_dbg_linear_cut(int32_t product, int64_t rows, int64_t k, int64_t n,
+                                      int32_t dtype, int32_t mixed, int32_t* tile_m,
+                                      int32_t* tile_n, int32_t* split);
+
 /* ------------------------------------------------------------------------ */
 /* Building blocks exposed for kernel-level checks                           */
 /* ------------------------------------------------------------------------ */

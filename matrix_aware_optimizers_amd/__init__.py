@@ -134,6 +134,8 @@ EXPORTS = {
                                             POINTER(Mat), Mat, c_void_p, c_size_t, c_void_p]),
     "mao_linear_backward_weight": (c_int32, [Mat, POINTER(Mat), POINTER(Q8C), c_int32, Mat,
                                              c_void_p, c_int32, c_void_p, c_size_t, c_void_p]),
+    "mao_dbg_linear_cut": (c_int32, [c_int32, c_int64, c_int64, c_int64, c_int32, c_int32,
+                                     POINTER(c_int32), POINTER(c_int32), POINTER(c_int32)]),
     "mao_gemm_nt": (c_int32, [c_int64, c_int64, c_int64, c_float, c_void_p, c_int64, c_void_p,
                               c_int64, c_int32, c_float, c_void_p, c_int64, c_void_p, c_int64,
                               c_int32, c_void_p]),

@@ -175,6 +175,10 @@ struct LinProblem {
   int a_km, b_km;
   LinEpilogue e;
 };
+struct LinCut {
+  int bm, bn, split;
+};
+LinCut lin_cut(int dtype, bool mixed, int64_t M, int64_t N, int64_t K);
 size_t lin_workspace(int dtype, int64_t M, int64_t N, int64_t K);
 // sums (weight gradient, or nullptr): lin_sum_rows x M floats that receive
 // partial column sums of A.

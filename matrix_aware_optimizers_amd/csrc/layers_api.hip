@@ -267,6 +267,22 @@ size_t mao_linear_backward_weight_workspace_size(int64_t rows, int64_t k, int64_
   return carve_weight(nullptr, rows, k, n, dtype, rebuilt != 0).bytes;
 }
 
+mao_status mao_dbg_linear_cut(int32_t product, int64_t rows, int64_t k, int64_t n, int32_t dtype,
+                              int32_t mixed, int32_t* tile_m, int32_t* tile_n, int32_t* split) {
+  if (!tile_m || !tile_n || !split) MAO_FAIL(MAO_E_NULL, "NULL result");
+  if (!sizes_ok(rows, k, n)) MAO_FAIL(MAO_E_SHAPE, "rows=%lld k=%lld n=%lld", (long long)rows, (long long)k, (long long)n);
+  if (!dtype_ok(dtype)) MAO_FAIL(MAO_E_DTYPE, "dtype=%d", dtype);
+  if (product < 0 || product > 2) MAO_FAIL(MAO_E_HPARAM, "product=%d", product);
+  const LinCut c = product == 0 && rows <= kTokenRows ? LinCut{16, 16, 1}
+                   : product == 0 ? lin_cut(dtype, mixed != 0, rows, n, k)
+                   : product == 1 ? lin_cut(dtype, mixed != 0, rows, k, n)
+                                  : lin_cut(dtype, false, n, k, rows);
+  *tile_m = c.bm;
+  *tile_n = c.bn;
+  *split = c.split;
+  return MAO_OK;
+}
+
 mao_status mao_linear(mao_mat X, mao_mat W, const void* bias, int32_t bias_dtype, int32_t act,
                       const mao_mat* residual, mao_mat Y, const mao_mat* preact, void* workspace,
                       size_t workspace_bytes, void* stream) {

@@ -108,6 +108,11 @@ Plan make_plan(int dtype, bool mixed, int64_t M, int64_t N, int64_t K) {
 
 }  // namespace
 
+LinCut lin_cut(int dtype, bool mixed, int64_t M, int64_t N, int64_t K) {
+  const Plan pl = make_plan(dtype, mixed, M, N, K);
+  return {kShapes[pl.cfg].bm, kShapes[pl.cfg].bn, pl.split};
+}
+
 size_t lin_workspace(int dtype, int64_t M, int64_t N, int64_t K) {
   // the caller may not know the result types yet
   if (dtype != MAO_BF16) return make_plan(dtype, false, M, N, K).ws;
