@@ -13,17 +13,19 @@
 // without a second read. Grids are persistent: gamma and beta stay in
 // registers, and the next row's loads are issued before the current row is
 // reduced. One wavefront per row up to 2048 columns (reductions stay inside
-// the wavefront: DPP adds and four lane reads, no LDS) in the forward pass; groups
-// of 256 to 1024 threads above, and in the backward pass from 513 columns on.
+// the wavefront: DPP adds and four lane reads, no LDS) in the forward pass, groups
+// of 256 to 1024 threads above; in the backward pass groups of 128 to 1024 threads from
+// 513 columns on.
 //
 // Measured (MI355X, bf16): forward 16384 x 1536 17.0 us, 101 MB, 5.9 TB/s (more than
-// a large copy's 5.2: they fit the 256 MB cache behind the L2); one row 5.9 us, the
-// kernel 3.4 of them. Backward with a joining gradient 16384 x 1536 44.3 us
+// a large copy's 5.2: they fit the 256 MB cache behind the L2); one row 5.9 to 6.4 us on
+// two cards, the kernel 3.4 of them. Backward with a joining gradient 16384 x 1536 44.3 us
 // (34.4 and 4.2 for the partial rows; 201 MB, 5.9 TB/s over the first); 4093 x 4096
-// from int8 codes 25.9 us (24.4 are the kernel, 84 MB, 3.5 TB/s: 16 rows
-// per workgroup are too few to hide each row's reduction, both sums in one exchange). Rows above 8192
-// columns hold two or four runs per thread and spill a few registers in the backward
-// pass.
+// from int8 codes 25.9 us (24.4 are the kernel, 84 MB, 3.5 TB/s: 16 rows per workgroup
+// are too few to hide each row's reduction, both sums in one exchange). fp32, 16384 x
+// 1536: forward 38.7 us, 201 MB, 5.2 TB/s, backward with a joining gradient 85 us, 403 MB,
+// 4.7 TB/s. Rows above 8192 columns hold two or four runs per thread and spill a few
+// registers in the backward pass (fp32 2000 x 8200 102 us, 262 MB, 2.6 TB/s).
 //
 // The column sums of the backward pass stay in registers over all rows a thread
 // group handles, are joined inside the workgroup in a fixed order, and leave

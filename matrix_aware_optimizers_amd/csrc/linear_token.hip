@@ -1,14 +1,15 @@
 // The linear layer's forward product for up to 16 rows (decoded tokens): y = act(x W^T
 // + b) + res.
 //
-// Bound: reading W once (one row, bf16: 1536 -> 6144 5.9 us, 3.6 of them the bytes at
-// the copy rate and the rest the launch, 512 -> 512 takes 3.7; 4096 -> 14336 22.3 us,
-// the copy rate). A workgroup takes 16 rows of W and all of K; its wavefronts take
-// 256-byte blocks of those rows in turn, straight from memory into registers in the
-// MFMA operand layout (16 x 16 results: W rows x tokens, so a wavefront's load is 64
-// contiguous bytes of each of 16 rows), the next block requested before the current
-// one is multiplied. x is small and comes from L2. The wavefronts' sums are joined
-// through LDS in a fixed order.
+// Bound: reading W once (one row, bf16, call after call on one stream: 1536 -> 6144 5.5 to
+// 5.9 us, 3.6 of them the bytes at the copy rate and the rest the launch, 512 -> 512 takes
+// 3.7; 4096 -> 14336 22.3 us, the copy rate; fp32 1536 -> 6144 10.7 us, 7.2 of them bytes.
+// By itself, under the profiler, the first takes 6.5: neighbours in a stream overlap.) A
+// workgroup takes 16 rows of W and all of K; its wavefronts take 256-byte blocks of those
+// rows in turn, straight from memory into registers in the MFMA operand layout (16 x 16
+// results: W rows x tokens, so a wavefront's load is 64 contiguous bytes of each of 16
+// rows), the next block requested before the current one is multiplied. x is small and
+// comes from L2. The wavefronts' sums are joined through LDS in a fixed order.
 //
 // 16 rows fill one MFMA result; the tile kernels take the rest. Timed against them
 // (this kernel : tiles, us, bf16): 1536 -> 6144 1 row 5.9 : 11.4, 16 rows 7.5 : 11.4;

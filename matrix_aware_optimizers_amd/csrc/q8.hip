@@ -9,7 +9,8 @@
 //
 // Measured (MI355X, 16384 x 6144 bf16, int8): 67 us to quantise and 68 to read back,
 // 305 MB each, 4.5 TB/s, against 5.2 of a large copy; 125 us for the pair where the
-// codes are read back from the cache behind the L2.
+// codes are read back from the cache behind the L2. fp32: 109 and 149 us, 507 MB each, 4.6
+// and 3.4 TB/s.
 #include "act.hpp"
 #include "layers.hpp"
 
@@ -19,7 +20,7 @@ namespace mao {
 
 namespace {
 
-// Work item w (16 columns) of a rows x nch grid of items, nch even.
+// Work item (16 columns, 8 of launch_act) of a rows x nch grid of items.
 struct Item {
   int row, c;
 };
