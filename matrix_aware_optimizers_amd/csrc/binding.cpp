@@ -12,6 +12,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/GradMode.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -236,10 +237,8 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
   try {
     return f();
   } catch (const Raised&) {
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-  } catch (...) {
-    PyErr_SetString(PyExc_RuntimeError, "unknown error");
+  } catch (...) {  // torch's own, out of memory among them, as torch raises them
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }

@@ -141,3 +141,16 @@ def test_vector_gradients_that_are_not_wanted(gpu_lib):
     assert call(torch.empty(72, device="cuda").data_ptr()) == 7  # MAO_E_WORKSPACE
     assert call(None) == 0
     assert torch.equal(out, want)
+
+
+def test_results_that_do_not_fit_memory(gpu_lib):
+    """torch's own error, which programs catch; the next call is unharmed."""
+    import torch
+    log("out of memory")
+    lib = gpu_lib
+    x = torch.randn((1 << 20, 8), device="cuda").bfloat16()
+    with pytest.raises(torch.OutOfMemoryError):
+        lib.linear(x, x)  # 2^40 results
+    y = lib.linear(x[:40], x[:24])
+    want = x[:40].double() @ x[:24].double().t().contiguous()
+    assert float((y.double() - want).abs().max()) < 0.1
