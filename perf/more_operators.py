@@ -267,10 +267,9 @@ def _moments(z, kind):
     return torch.cat([mean, 1.0 / torch.sqrt((d * d).mean(dim=1, keepdim=True) + NORM_EPS)], dim=1)
 
 
-# An 8-bit state's value is scale * F(code). F has a 4-bit exponent: with 3 (first moment,
-# and a sign in the top bit) or 4 bits of mantissa, F(c) is the float whose bits are
-# (c << (23 - mantissa)) + BASE, F(0) = 0; the largest code's F is TOP.
-BASE = 112 << 23
+# An 8-bit state's value is scale * F(code). F is a float with an exponent of 4 bits (bias
+# 15, subnormals for exponent 0) and a mantissa of 3 bits (first moment, whose top bit is
+# the sign) or 4; the largest F is TOP.
 MANTISSA = {"m": 3, "v": 4}
 TOP = {"m": 1.875, "v": 1.9375}
 TINY = 2.0 ** -100  # a span whose largest magnitude is below it counts as zeros
@@ -281,8 +280,10 @@ DITHER = {"m": (0x9E3779B9, 0xC13FA9A9), "v": (0xC13FA9A9, 0x9E3779B9)}
 def _decode(codes, scale, which):
     code = codes.int()
     mag = code & 127 if which == "m" else code
-    f = ((mag << (23 - MANTISSA[which])) + BASE).view(torch.float32)
-    f = torch.where(mag == 0, torch.zeros_like(f), f)
+    k = MANTISSA[which]
+    e = mag >> k
+    f = ((mag & ((1 << k) - 1)) + torch.where(e > 0, 1 << k, 0)).float()
+    f = f * torch.exp2((e.clamp(min=1) - (15 + k)).float())
     if which == "m":
         f = torch.where(code > 127, -f, f)
     return f * scale.repeat_interleave(SPAN)[:code.numel()]
@@ -302,7 +303,10 @@ def _encode(x, which, t):
     i = torch.arange(spans * SPAN, device=x.device).view(spans, SPAN)
     drop = 23 - MANTISSA[which]
     d = ((i * first + t * second) & 0xFFFFFFFF) >> (32 - drop)
-    code = (y.view(torch.int32).long() - BASE + d) >> drop
+    # places of the code, then those that the dither rounds away
+    normal = y.view(torch.int32).long() - (112 << 23)
+    places = torch.where(y < 2.0 ** -14, (y * 2.0 ** 37).long(), normal)
+    code = (places + d) >> drop
     low = 0 if which == "m" else 1
     code = torch.where((a > 0) & live, code.clamp(low, 127 if which == "m" else 255), 0)
     code = code.view(-1)[:n]
@@ -517,9 +521,9 @@ def work(case):
 
 def _exact_float(codes, mantissa):
     """F of codes in 64 bits, by its exponent and mantissa."""
-    e = torch.div(codes, 1 << mantissa, rounding_mode="floor").double() - 15.0
+    e = torch.div(codes, 1 << mantissa, rounding_mode="floor").double()
     f = (codes % (1 << mantissa)).double() / (1 << mantissa)
-    return torch.where(codes == 0, torch.zeros_like(e), torch.exp2(e) * (1.0 + f))
+    return torch.where(e == 0, f * 2.0 ** -14, torch.exp2(e - 15.0) * (1.0 + f))
 
 
 def _exact_store(x, which):
@@ -530,7 +534,7 @@ def _exact_store(x, which):
     scale = largest / (2.0 - 0.5 ** mant)
     y = pad / scale
     # within its binade: the step below y, and y's place between two steps
-    e = torch.floor(torch.log2(y))
+    e = torch.floor(torch.log2(y)).clamp(min=-14.0)
     place = (y * torch.exp2(-e) - 1.0) * (1 << mant)
     first, second = DITHER[which]
     i = torch.arange(pad.numel(), device=x.device).view(-1, SPAN)
