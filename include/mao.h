@@ -402,6 +402,55 @@ MAO_API mao_status adamw_step(void* w, int32_t w_dtype, const void* g, int32_t g
                       float* v, int64_t n, int64_t t, float lr, float beta1, float beta2,
                       float eps, float weight_decay, float* update_out, void* stream);
 
+/* State of one tensor of adamw_step_many. */
+typedef enum {
+  MAO_ADAM_F32 = 0,  /* m, v: n floats each */
+  MAO_ADAM_8BIT = 1  /* m, v: n codes of one byte each, with a float scale per 256 */
+} mao_adam_state;
+
+/* One tensor of adamw_step_many: n contiguous elements each of w, g, m and v, each aligned
+ * to its elements only (tensors may lie back to back in one buffer). 8-bit states: m holds
+ * m_scale[i / 256] F3(code), v holds (v_scale[i / 256] F4(code))^2, where F3 is a float with
+ * a sign, a 4-bit exponent (bias 15, subnormals) and a 3-bit mantissa, F4 one with no sign
+ * and a 4-bit mantissa. All zero bytes (scales too) are the initial state. Scales: ceil(n /
+ * 256) floats each; NULL with fp32 states. n = 0: nothing is done. */
+typedef struct {
+  void* w;
+  const void* g;
+  void *m, *v;
+  float *m_scale, *v_scale;
+  int64_t n;
+  int32_t w_dtype, g_dtype; /* mao_dtype */
+  int32_t state;            /* mao_adam_state */
+  float lr, weight_decay;   /* of this tensor, >= 0 */
+} mao_adamw_tensor;
+
+/*
+ * adamw_step_many -- adamw_step on `count` tensors (1..4096, MAO_E_SHAPE otherwise), each
+ * with its own learning rate, weight decay and kind of state, and every gradient multiplied by
+ * *grad_scale (a device float: a clipping or loss-scaling factor; NULL: 1). tensors: host
+ * memory, read during the call. A tensor with fp32 states gets what adamw_step gives. No
+ * buffer that is written may overlap another one (MAO_E_ALIAS: a tensor listed twice).
+ * 8-bit states are rounded up or down by a fixed dither of element index and t, unbiased over
+ * the steps, so that averages move by less than a code's step too. 256 elements whose m or v
+ * holds a NaN or an infinity read as NaN from then on.
+ */
+MAO_API mao_status adamw_step_many(int32_t count, const mao_adamw_tensor* tensors, int64_t t,
+                                   float beta1, float beta2, float eps, const float* grad_scale,
+                                   void* stream);
+
+/* The values of an 8-bit state: m_out, v_out <- m, v (n elements of the call's dtype). */
+typedef struct {
+  const void *m, *v;
+  const float *m_scale, *v_scale;
+  void *m_out, *v_out;
+  int64_t n;
+} mao_adamw8_state;
+
+/* mao_adamw8_read -- the values of `count` (1..4096) 8-bit states, as bf16 or fp32. */
+MAO_API mao_status mao_adamw8_read(int32_t count, const mao_adamw8_state* states, int32_t dtype,
+                                   void* stream);
+
 /* ------------------------------------------------------------------------ */
 /* Layer operators: what makes the gradients that the steps consume           */
 /* ------------------------------------------------------------------------ */

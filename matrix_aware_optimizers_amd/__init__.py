@@ -72,6 +72,20 @@ class Q8C(ctypes.Structure):
                 ("ld", c_int64), ("ld_scale", c_int64), ("format", c_int32)]
 
 
+class AdamwTensorC(ctypes.Structure):
+    _fields_ = [("w", c_void_p), ("g", c_void_p), ("m", c_void_p), ("v", c_void_p),
+                ("m_scale", c_void_p), ("v_scale", c_void_p), ("n", c_int64),
+                ("w_dtype", c_int32), ("g_dtype", c_int32), ("state", c_int32), ("lr", c_float),
+                ("weight_decay", c_float)]
+
+
+class Adamw8StateC(ctypes.Structure):
+    _fields_ = [("m", c_void_p), ("v", c_void_p), ("m_scale", c_void_p), ("v_scale", c_void_p),
+                ("m_out", c_void_p), ("v_out", c_void_p), ("n", c_int64)]
+
+
+ADAM_STATES = {"f32": 0, "8bit": 1}
+ADAM_SPAN = 256
 REFRESH_MODES = {"qr": 0, "eigh": 1}
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 Q8_FORMATS = {"int8": 0, "e4m3": 1}
@@ -116,6 +130,9 @@ EXPORTS = {
     "adamw_step": (c_int32, [c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_void_p, c_int64,
                              c_int64, c_float, c_float, c_float, c_float, c_float, c_void_p,
                              c_void_p]),
+    "adamw_step_many": (c_int32, [c_int32, POINTER(AdamwTensorC), c_int64, c_float, c_float, c_float,
+                                  c_void_p, c_void_p]),
+    "mao_adamw8_read": (c_int32, [c_int32, POINTER(Adamw8StateC), c_int32, c_void_p]),
     "mao_q8_quantize": (c_int32, [Mat, POINTER(Q8C), c_void_p]),
     "mao_q8_dequantize": (c_int32, [POINTER(Q8C), c_int32, Mat, c_void_p]),
     "mao_layer_norm": (c_int32, [Mat, c_void_p, c_void_p, c_int32, c_float, Mat, c_void_p,
@@ -624,6 +641,36 @@ def linear_backward_weight(dY, X, *, x_act="none", dtype=None, out=None, dbias=N
         raise ValueError("accumulate needs out and dbias")
     return _run("linear_backward_weight", dY, X, _act(x_act), _result_type(dtype, F32), out, dbias,
                 bool(accumulate))
+
+
+def adamw8_state(w):
+    """A zero 8-bit AdamW state for the tensor w: (m, m_scale, v, v_scale), codes shaped like
+    w and one float scale per 256 elements."""
+    torch = _torch()
+    blocks = (w.numel() + ADAM_SPAN - 1) // ADAM_SPAN
+    codes = dict(dtype=torch.uint8, device=w.device)
+    scales = dict(dtype=torch.float32, device=w.device)
+    return (torch.zeros(w.shape, **codes), torch.zeros(blocks, **scales),
+            torch.zeros(w.shape, **codes), torch.zeros(blocks, **scales))
+
+
+def adamw_step_many(items, t: int, *, lr, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.0,
+                    grad_scale=None):
+    """adamw_step on many tensors in one call. ``items``: tuples (w, g, m, v) with fp32 states
+    or (w, g, m, m_scale, v, v_scale) with 8-bit ones (``adamw8_state``), contiguous tensors
+    of one device. ``lr`` and ``weight_decay``: a number, or a list with one per tensor.
+    ``grad_scale``: a device fp32 scalar that every gradient is multiplied by."""
+    if len(items) == 0:
+        raise ValueError("adamw_step_many needs at least one tensor")
+    _run("adamw_step_many", items[0][0], items, t, lr, beta1, beta2, eps, weight_decay, grad_scale)
+
+
+def adamw8_read(states, dtype=None, out=None):
+    """[(m, v), ...]: the values that 8-bit states (m, m_scale, v, v_scale) hold, as fp32
+    (``dtype`` or the tensors of ``out``: bf16 too)."""
+    if len(states) == 0:
+        raise ValueError("adamw8_read needs at least one state")
+    return _run("adamw8_read", states[0][0], states, _result_type(dtype, F32), out)
 
 
 def _as_batch(X):

@@ -1,4 +1,5 @@
-// Argument marshalling of the layer operators: torch tensors to the C ABI's views.
+// Argument marshalling of the layer operators and of the many-tensor AdamW step: torch
+// tensors to the C ABI's views.
 //
 // These calls are made per layer and, decoding, per token, so the look at each
 // tensor and the allocation of results happen here rather than in Python (a
@@ -15,7 +16,10 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <exception>
+#include <memory>
+#include <vector>
 
 #include "../../include/mao.h"
 
@@ -402,6 +406,180 @@ PyObject* linear_backward_weight(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The elements of a tensor that an optimizer step reads or writes in place (autograd looks on
+// at none of it, as with the other steps).
+struct Flat {
+  void* p = nullptr;
+  int64_t n = 0;
+  at::ScalarType type;
+  Flat(PyObject* o, int64_t dev) {
+    const at::Tensor& t = tensor(o);
+    if (!t.is_contiguous()) fail(PyExc_ValueError, "adamw_step_many needs contiguous tensors");
+    on_device(t, dev);
+    p = t.data_ptr();
+    n = t.numel();
+    type = t.scalar_type();
+  }
+  void want(at::ScalarType ty, int64_t size, const char* name) const {
+    if (type != ty) {
+      PyErr_Format(PyExc_TypeError, "%s must be %s", name,
+                   ty == at::kFloat ? "float32" : ty == at::kByte ? "uint8" : "bfloat16");
+      throw Raised{};
+    }
+    if (n != size) {
+      PyErr_Format(PyExc_ValueError, "%s needs %lld elements, not %lld", name, (long long)size,
+                   (long long)n);
+      throw Raised{};
+    }
+  }
+  int32_t code() const {
+    if (type == at::kFloat) return MAO_F32;
+    if (type == at::kBFloat16) return MAO_BF16;
+    fail(PyExc_TypeError, "unsupported dtype: float32 or bfloat16 is needed");
+  }
+};
+
+// A list or tuple, held for the call.
+struct Sequence {
+  PyObject* s;
+  explicit Sequence(PyObject* o, const char* what) : s(PySequence_Fast(o, what)) {
+    if (!s) throw Raised{};
+  }
+  ~Sequence() { Py_DECREF(s); }
+  Sequence(const Sequence&) = delete;
+  int64_t size() const { return PySequence_Fast_GET_SIZE(s); }
+  PyObject* operator[](int64_t i) const { return PySequence_Fast_GET_ITEM(s, i); }
+};
+
+// A number for all tensors, or one for each.
+struct Numbers {
+  float one = 0.f;
+  std::vector<float> each;
+  Numbers(PyObject* o, int64_t n, const char* name) {
+    if (PyList_Check(o) || PyTuple_Check(o)) {
+      const Sequence q(o, name);
+      if (q.size() != n) {
+        PyErr_Format(PyExc_ValueError, "%s: %lld values for %lld tensors", name,
+                     (long long)q.size(), (long long)n);
+        throw Raised{};
+      }
+      for (int64_t i = 0; i < n; ++i) each.push_back(number(q[i]));
+    } else {
+      one = number(o);
+    }
+  }
+  static float number(PyObject* o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw Raised{};
+    return (float)v;
+  }
+  float operator[](int64_t i) const { return each.empty() ? one : each[(size_t)i]; }
+};
+
+constexpr int64_t kSpan = 256;  // elements per scale of an 8-bit state
+
+// (first weight, items, t, lr, beta1, beta2, eps, weight_decay, grad_scale, device, stream):
+// items of (w, g, m, v) or (w, g, m, m_scale, v, v_scale)
+PyObject* adamw_step_many(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 11, [&]() -> PyObject* {
+    const int64_t dev = integer(a[9]);
+    const Sequence items(a[1], "expected a list of tensors' tuples");
+    const int64_t count = items.size();
+    const Numbers lr(a[3], count, "lr"), wd(a[7], count, "weight_decay");
+    std::vector<mao_adamw_tensor> t((size_t)count);
+    for (int64_t i = 0; i < count; ++i) {
+      const Sequence q(items[i], "expected a tuple of tensors");
+      if (q.size() != 4 && q.size() != 6)
+        fail(PyExc_ValueError, "expected (w, g, m, v) or (w, g, m, m_scale, v, v_scale)");
+      const bool q8 = q.size() == 6;
+      const Flat w(q[0], dev), g(q[1], dev), m(q[2], dev), v(q[q8 ? 4 : 3], dev);
+      if (g.n != w.n) fail(PyExc_ValueError, "w and g of different sizes");
+      m.want(q8 ? at::kByte : at::kFloat, w.n, "m");
+      v.want(q8 ? at::kByte : at::kFloat, w.n, "v");
+      mao_adamw_tensor& x = t[(size_t)i];
+      x = mao_adamw_tensor{w.p, g.p, m.p, v.p, nullptr, nullptr, w.n, w.code(), g.code(),
+                           q8 ? MAO_ADAM_8BIT : MAO_ADAM_F32, lr[i], wd[i]};
+      if (q8) {
+        const Flat ms(q[3], dev), vs(q[5], dev);
+        ms.want(at::kFloat, (w.n + kSpan - 1) / kSpan, "m_scale");
+        vs.want(at::kFloat, (w.n + kSpan - 1) / kSpan, "v_scale");
+        x.m_scale = (float*)ms.p;
+        x.v_scale = (float*)vs.p;
+      }
+    }
+    const float* gs = nullptr;
+    if (a[8] != Py_None) {
+      const Flat f(a[8], dev);
+      f.want(at::kFloat, 1, "grad_scale");
+      gs = (const float*)f.p;
+    }
+    check(adamw_step_many((int32_t)std::min<int64_t>(count, INT32_MAX), t.data(), integer(a[2]),
+                          Numbers::number(a[4]), Numbers::number(a[5]), Numbers::number(a[6]), gs,
+                          (void*)integer(a[10])),
+          "adamw_step_many");
+    Py_RETURN_NONE;
+  });
+}
+
+// (first code tensor, states, type, out, device, stream): states of (m, m_scale, v, v_scale),
+// out a list of (m, v) -> None, or None -> a list of (m, v)
+PyObject* adamw8_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 6, [&]() -> PyObject* {
+    const int64_t dev = integer(a[4]);
+    const Sequence states(a[1], "expected a list of states");
+    const int64_t count = states.size();
+    std::vector<mao_adamw8_state> t((size_t)count);
+    std::vector<at::Tensor> made;
+    at::ScalarType type = type_of(integer(a[2]));
+    const bool given = a[3] != Py_None;
+    std::vector<std::unique_ptr<Sequence>> outs;
+    if (given) {
+      const Sequence o(a[3], "out must be a list of (m, v)");
+      if (o.size() != count) fail(PyExc_ValueError, "out must hold one (m, v) for each state");
+      for (int64_t i = 0; i < count; ++i) {
+        outs.emplace_back(new Sequence(o[i], "out must be a list of (m, v)"));
+        if (outs.back()->size() != 2) fail(PyExc_ValueError, "out must be a list of (m, v)");
+      }
+      if (count > 0) type = tensor((*outs[0])[0]).scalar_type();
+    }
+    if (type != at::kFloat && type != at::kBFloat16)
+      fail(PyExc_TypeError, "unsupported dtype: float32 or bfloat16 is needed");
+    for (int64_t i = 0; i < count; ++i) {
+      const Sequence q(states[i], "expected a tuple (m, m_scale, v, v_scale)");
+      if (q.size() != 4) fail(PyExc_ValueError, "expected a tuple (m, m_scale, v, v_scale)");
+      const Flat m(q[0], dev), ms(q[1], dev), v(q[2], dev), vs(q[3], dev);
+      m.want(at::kByte, m.n, "m");
+      v.want(at::kByte, m.n, "v");
+      ms.want(at::kFloat, (m.n + kSpan - 1) / kSpan, "m_scale");
+      vs.want(at::kFloat, (m.n + kSpan - 1) / kSpan, "v_scale");
+      void* to[2];
+      for (int k = 0; k < 2; ++k) {
+        if (given) {
+          const Flat o((*outs[(size_t)i])[k], dev);
+          o.want(type, m.n, "out");
+          to[k] = o.p;
+        } else {
+          const at::Tensor& like = tensor(q[0]);
+          made.push_back(at::empty(like.sizes(), like.options().dtype(type)));
+          to[k] = made.back().data_ptr();
+        }
+      }
+      t[(size_t)i] = mao_adamw8_state{m.p, v.p, (const float*)ms.p, (const float*)vs.p,
+                                      to[0], to[1], m.n};
+    }
+    check(mao_adamw8_read((int32_t)std::min<int64_t>(count, INT32_MAX), t.data(),
+                          type == at::kBFloat16 ? MAO_BF16 : MAO_F32, (void*)integer(a[5])),
+          "mao_adamw8_read");
+    if (given) return Py_NewRef(a[3]);
+    PyObject* list = PyList_New(count);
+    if (!list) throw Raised{};
+    for (int64_t i = 0; i < count; ++i)
+      PyList_SET_ITEM(list, i, Py_BuildValue("NN", THPVariable_Wrap(made[(size_t)(2 * i)]),
+                                             THPVariable_Wrap(made[(size_t)(2 * i + 1)])));
+    return list;
+  });
+}
+
 #define MAO_METHOD(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {MAO_METHOD(init),
                            MAO_METHOD(q8_quantize),
@@ -411,6 +589,8 @@ PyMethodDef g_methods[] = {MAO_METHOD(init),
                            MAO_METHOD(linear),
                            MAO_METHOD(linear_backward_input),
                            MAO_METHOD(linear_backward_weight),
+                           MAO_METHOD(adamw_step_many),
+                           MAO_METHOD(adamw8_read),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_layers", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

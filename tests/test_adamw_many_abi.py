@@ -1,0 +1,148 @@
+"""Refusals of the many-tensor AdamW step (host only), and the 8-bit states' oracle.
+
+Invalid calls use fake, never-dereferenced device addresses, as in test_abi.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+
+import matrix_aware_optimizers_amd as mao
+from oracle import adam8
+from tests.test_abi import E_ALIAS, E_DTYPE, E_HPARAM, E_LAYOUT, E_NULL, E_SHAPE, FAKE, needs_no_gpu
+
+MB = 1 << 20
+
+
+def item(k=0, n=1000, state=0, wd=0, gd=0, lr=1e-3, decay=0.0, **at):
+    a = {name: FAKE + (8 * k + j) * MB for j, name in enumerate(("w", "g", "m", "v", "ms", "vs"))}
+    a.update(at)
+    return mao.AdamwTensorC(a["w"], a["g"], a["m"], a["v"], a["ms"], a["vs"], n, wd, gd, state, lr,
+                            decay)
+
+
+def step(items, t=1, b1=0.9, b2=0.95, eps=1e-8, gs=None, count=None):
+    arr = (mao.AdamwTensorC * max(1, len(items)))(*items) if items is not None else None
+    return mao.load().adamw_step_many(len(items or []) if count is None else count, arr, t, b1, b2,
+                                      eps, gs, None)
+
+
+@needs_no_gpu
+def test_step_refusals():
+    assert step(None, count=1) == E_NULL
+    assert step([]) == E_SHAPE
+    assert step([item()], count=4097) == E_SHAPE
+    assert step([item(n=-1)]) == E_SHAPE
+    assert step([item(n=(1 << 40) + 1)]) == E_SHAPE
+    for name in ("w", "g", "m", "v"):
+        assert step([item(**{name: None})]) == E_NULL
+        assert step([item(**{name: FAKE + 2})]) == E_LAYOUT  # fp32 at a half-word
+    assert step([item(state=1, ms=None)]) == E_NULL
+    assert step([item(state=1, vs=FAKE + 5 * MB + 1)]) == E_LAYOUT
+    assert step([item(state=2)]) == E_DTYPE
+    assert step([item(wd=2)]) == E_DTYPE
+    assert step([item(gd=-1)]) == E_DTYPE
+    assert step([item()], t=0) == E_HPARAM
+    assert step([item()], b1=1.0) == E_HPARAM
+    assert step([item()], b2=-0.1) == E_HPARAM
+    assert step([item()], b2=float("nan")) == E_HPARAM
+    assert step([item()], eps=0.0) == E_HPARAM
+    assert step([item(lr=-1.0)]) == E_HPARAM
+    assert step([item(decay=float("inf"))]) == E_HPARAM
+    assert step([item()], gs=ctypes.c_void_p(FAKE + 50 * MB + 2)) == E_LAYOUT
+
+
+@needs_no_gpu
+def test_step_aliases():
+    """No written buffer may share a byte with another; gradients may be shared."""
+    assert step([item(0), item(1, w=FAKE + 999 * 4)]) == E_ALIAS  # last element of w
+    assert step([item(0), item(0)]) == E_ALIAS  # one tensor twice
+    assert step([item(0, g=FAKE)]) == E_ALIAS
+    assert step([item(0, v=FAKE + 2 * MB + 4)]) == E_ALIAS
+    assert step([item(0, state=1, vs=FAKE + 4 * MB + 12)]) == E_ALIAS  # 4 scales of 1000
+    assert step([item(0), item(1, g=FAKE + 3 * MB + 400)]) == E_ALIAS  # g read where v is written
+    assert step([item(0)], gs=ctypes.c_void_p(FAKE + 2 * MB)) == E_ALIAS
+    # many tensors: the same check on a sorted list that does not fit the stack
+    many = [item(k) for k in range(300)]
+    many[299] = item(299, m=FAKE + 17 * 8 * MB + 3 * MB)
+    assert step(many) == E_ALIAS
+
+
+@needs_no_gpu
+def test_read_refusals():
+    def read(n=1000, dtype=0, count=1, null=False, **at):
+        a = {k: FAKE + j * MB for j, k in enumerate(("m", "v", "ms", "vs", "mo", "vo"))}
+        a.update(at)
+        s = (mao.Adamw8StateC * 1)(mao.Adamw8StateC(a["m"], a["v"], a["ms"], a["vs"], a["mo"],
+                                                    a["vo"], n))
+        return mao.load().mao_adamw8_read(count, None if null else s, dtype, None)
+
+    assert read(null=True) == E_NULL
+    assert read(count=0) == E_SHAPE
+    assert read(n=-2) == E_SHAPE
+    assert read(dtype=3) == E_DTYPE
+    for k in ("m", "v", "ms", "vs", "mo", "vo"):
+        assert read(**{k: None}) == E_NULL
+    assert read(mo=FAKE + 4 * MB + 2) == E_LAYOUT
+    assert read(ms=FAKE + 2 * MB + 2) == E_LAYOUT
+    assert read(vo=FAKE + 4 * MB + 3996) == E_ALIAS
+    assert read(mo=FAKE) == E_ALIAS
+
+
+def test_binding_refusals():
+    """Shapes, types and devices that the C call cannot see."""
+    torch = pytest.importorskip("torch")
+    w = torch.zeros(300)
+    with pytest.raises(ValueError):
+        mao.adamw_step_many([], 1, lr=1e-3)
+    with pytest.raises(ValueError):
+        mao.adamw8_read([])
+    with pytest.raises(ValueError):  # host tensors
+        mao.adamw_step_many([(w, w, w, w)], 1, lr=1e-3)
+    with pytest.raises(TypeError):
+        mao.adamw8_read([mao.adamw8_state(w)], dtype=torch.float16)
+    m, ms, v, vs = mao.adamw8_state(torch.zeros((3, 100)))
+    assert m.shape == v.shape == (3, 100) and ms.shape == vs.shape == (2,)
+    assert m.dtype == v.dtype == torch.uint8 and ms.dtype == vs.dtype == torch.float32
+
+
+@pytest.mark.parametrize("which,top,smallest", [("m", 1.875, 2.0 ** -17), ("v", 1.9375, 2.0 ** -18)])
+def test_oracle_codes(which, top, smallest):
+    """The values of all codes rise, by at most 1/8 (1/16) of themselves above the
+    subnormals; the largest and the smallest are as the format says."""
+    n = 128 if which == "m" else 256
+    f = adam8.code_value(np.arange(n), which)
+    assert f[0] == 0 and f[1] == smallest and f[-1] == top
+    assert (np.diff(f) > 0).all()
+    normal = np.arange(1 << adam8.MANTISSA[which], n)
+    assert (np.diff(f[normal]) / f[normal][:-1] <= 0.5 ** adam8.MANTISSA[which]).all()
+
+
+@pytest.mark.parametrize("which", ["m", "v"])
+def test_oracle_round_trip_and_average(which):
+    """What the codes stand for is stored without change; anything else as one of its two
+    neighbours, and as itself on average over the steps. The average of N terms of the
+    recurrence is off by its discrepancy, which for N = 512 is below 0.02 for both
+    sequences (its largest gap between sorted points plus their unevenness, computed
+    here)."""
+    r = np.random.default_rng(5)
+    top = 1.875 if which == "m" else 1.9375
+    n = 128 if which == "m" else 256
+    grid = adam8.code_value(np.arange(n), which)
+    codes, scales = adam8.encode(grid, which, 9)
+    assert (codes == np.arange(n)).all() and scales[0] == grid[-1] / top
+    steps = 512
+    pts = np.sort([adam8.dither(1, which, t)[0] for t in range(1, steps + 1)])
+    i = np.arange(steps)
+    disc = max(np.max((i + 1) / steps - pts), np.max(pts - i / steps))
+    assert disc < 0.02
+    x = np.concatenate([[1.0], np.exp(r.uniform(np.log(1e-3), 0.0, 60))])
+    total = np.zeros_like(x)
+    for t in range(1, steps + 1):
+        c, s = adam8.encode(x, which, t)
+        v = adam8.decode(c, s, which)
+        step = np.maximum(2.0 ** np.floor(np.log2(x * top)), 2.0 ** -14) / top / 2 ** adam8.MANTISSA[which]
+        assert (np.abs(v - x) <= step * (1 + 1e-12)).all()
+        total += v
+    # an element's dithers are the sequence shifted by its index: the same discrepancy times 2
+    assert (np.abs(total / steps - x) <= 2 * disc * step).all()
