@@ -430,7 +430,8 @@ typedef struct {
  * with its own learning rate, weight decay and kind of state, and every gradient multiplied by
  * *grad_scale (a device float: a clipping or loss-scaling factor; NULL: 1). tensors: host
  * memory, read during the call. A tensor with fp32 states gets what adamw_step gives. No
- * buffer that is written may overlap another one (MAO_E_ALIAS: a tensor listed twice).
+ * buffer that is written may overlap another one (MAO_E_ALIAS: a tensor listed twice). n is at
+ * most 2^34.
  * 8-bit states are rounded up or down by a fixed dither of element index and t, unbiased over
  * the steps, so that averages move by less than a code's step too. 256 elements whose m or v
  * holds a NaN or an infinity read as NaN from then on.
@@ -583,6 +584,50 @@ MAO_API mao_status mao_linear_backward_weight(mao_mat dY, const mao_mat* X, cons
                                               int32_t x_act, mao_mat dW, float* dbias,
                                               int32_t accumulate, void* workspace,
                                               size_t workspace_bytes, void* stream);
+
+/*
+ * Log probabilities of tokens: X holds rows of logits (rows x vocabulary, bf16 or fp32), the
+ * results of mao_linear for a model's head. targets: one token (int64) per row; below 0: the
+ * row has none (log probability 0, no gradient); at or above the vocabulary's size: NaN. A
+ * masked logit is -inf: probability 0. A row of nothing else has log probabilities of -inf,
+ * entropy 0 and no gradient; one with a NaN or +inf has NaN results.
+ */
+
+/* Workspace bytes (0 when none is needed or an argument is invalid). */
+MAO_API size_t mao_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int32_t top);
+
+/*
+ * mao_token_logprobs -- with M = max_j x_j and S = sum_j e^(x_j - M) of each row:
+ *   logprob = (x_target - M) - log S;  entropy = -sum_j p_j log p_j;
+ *   stats = (M, log S), which add up to the log of the sum of exponentials;
+ *   top_logprobs, top_ids (rows x top): the `top` (0..32, at most the vocabulary's size:
+ *   MAO_E_HPARAM) most likely tokens, equal ones by their number (NaN and -1 in a row of NaN).
+ * Each result NULL if it is not wanted; logprob goes with targets, the alternatives with top.
+ */
+MAO_API mao_status mao_token_logprobs(mao_mat X, const int64_t* targets, float* logprob,
+                                      float* entropy, float* stats, int32_t top,
+                                      float* top_logprobs, int64_t* top_ids, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/*
+ * mao_token_logprobs_backward -- from the gradients of logprob, entropy and lse = M + log S
+ * (each NULL or rows floats, one at least):
+ *   dX_j = dlogprob (d_jt - p_j) + dlse p_j - dentropy p_j (log p_j + entropy)
+ * stats (and entropy, with dentropy) as mao_token_logprobs gave them. dX: bf16 or fp32, may be
+ * X itself. A row whose gradients are all 0 gets zeros whatever it holds.
+ */
+MAO_API mao_status mao_token_logprobs_backward(mao_mat X, const int64_t* targets,
+                                               const float* stats, const float* entropy,
+                                               const float* dlogprob, const float* dentropy,
+                                               const float* dlse, mao_mat dX, void* stream);
+
+/*
+ * mao_token_loss -- logprob (NULL or rows floats) and the gradient of the loss
+ * sum over rows of -weight logprob, in one pass: dX_j = weight (p_j - d_jt). weight: NULL (1)
+ * or rows floats. dX: bf16 or fp32, may be X itself. A row without a target is not read.
+ */
+MAO_API mao_status mao_token_loss(mao_mat X, const int64_t* targets, const float* weight,
+                                  float* logprob, mao_mat dX, void* stream);
 
 /* Test hook: the tile shape and the K split that a linear product of these sizes is cut
  * into. product: 0 forward, 1 input gradient, 2 weight gradient; mixed != 0: a bf16

@@ -17,6 +17,7 @@ from __future__ import annotations
 import ctypes
 import os
 from ctypes import POINTER, c_float, c_int32, c_int64, c_size_t, c_void_p
+from typing import NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmao.so")
@@ -151,6 +152,12 @@ EXPORTS = {
                                             POINTER(Mat), Mat, c_void_p, c_size_t, c_void_p]),
     "mao_linear_backward_weight": (c_int32, [Mat, POINTER(Mat), POINTER(Q8C), c_int32, Mat,
                                              c_void_p, c_int32, c_void_p, c_size_t, c_void_p]),
+    "mao_token_logprobs_workspace_size": (c_size_t, [c_int64, c_int64, c_int32]),
+    "mao_token_logprobs": (c_int32, [Mat, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p,
+                                     c_void_p, c_void_p, c_size_t, c_void_p]),
+    "mao_token_logprobs_backward": (c_int32, [Mat, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                              c_void_p, Mat, c_void_p]),
+    "mao_token_loss": (c_int32, [Mat, c_void_p, c_void_p, c_void_p, Mat, c_void_p]),
     "mao_dbg_linear_cut": (c_int32, [c_int32, c_int64, c_int64, c_int64, c_int32, c_int32,
                                      POINTER(c_int32), POINTER(c_int32), POINTER(c_int32)]),
     "mao_gemm_nt": (c_int32, [c_int64, c_int64, c_int64, c_float, c_void_p, c_int64, c_void_p,
@@ -641,6 +648,40 @@ def linear_backward_weight(dY, X, *, x_act="none", dtype=None, out=None, dbias=N
         raise ValueError("accumulate needs out and dbias")
     return _run("linear_backward_weight", dY, X, _act(x_act), _result_type(dtype, F32), out, dbias,
                 bool(accumulate))
+
+
+class TokenLogprobs(NamedTuple):
+    """Results of token_logprobs: per row the target's log probability, the entropy, (maximum,
+    log of the sum) and the most likely alternatives."""
+    logprob: object
+    entropy: object
+    stats: object
+    top_logprobs: object
+    top_ids: object
+
+
+def token_logprobs(X, targets=None, *, top=0, entropy=True) -> TokenLogprobs:
+    """Log probabilities of the rows of logits X (bf16 or fp32): of ``targets`` (int64, one per
+    row; below 0: none, 0 comes back), with the entropy and the ``top`` (up to 32) most likely
+    tokens, equal ones by their number. ``stats`` (rows x 2) is what the backward call needs;
+    its columns add up to the log of the sum of exponentials. None for what is not asked for."""
+    return TokenLogprobs(*_run("token_logprobs", X, targets, bool(entropy), top))
+
+
+def token_logprobs_backward(X, targets, stats, *, dlogprob=None, dentropy=None, dlse=None,
+                            entropy=None, out=None):
+    """The gradient of the logits X from those of the log probabilities, the entropy (with its
+    value, ``entropy``) and the log of the sum of exponentials. ``out`` may be X."""
+    return _run("token_logprobs_backward", X, targets, stats, entropy, dlogprob, dentropy, dlse, out)
+
+
+def token_loss(X, targets, weight=None, *, out=None):
+    """(logprob, dX): the targets' log probabilities and the gradient of the loss
+    -(weight * logprob).sum(), in one pass over the logits X. ``weight``: fp32, one per row (1 if
+    not given). ``out`` may be X, which the gradient then replaces."""
+    if targets is None:
+        raise ValueError("token_loss needs targets")
+    return _run("token_loss", X, targets, weight, out)
 
 
 def adamw8_state(w):

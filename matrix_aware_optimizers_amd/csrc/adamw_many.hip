@@ -190,7 +190,7 @@ struct Spans {
 };
 
 constexpr int kMostTensors = 4096;
-constexpr int64_t kMostElements = (int64_t)1 << 40;
+constexpr int64_t kMostElements = (int64_t)1 << 34;
 
 mao_status check_count(int32_t count, const void* items) {
   if (!items) MAO_FAIL(MAO_E_NULL, "tensors is NULL");
@@ -219,8 +219,8 @@ mao_status go(const AdamTable& a, bool state8, uint32_t blocks, hipStream_t s) {
   return MAO_OK;
 }
 
-// One launch's table, sent off when it is full or its grid is.
-constexpr int64_t kMostBlocks = (int64_t)1 << 30;
+// One launch's table, sent off when it is full or its grid is (2^32 threads).
+constexpr int64_t kMostBlocks = (1 << 24) - 1;
 
 mao_status send(AdamTable& a, int kind, int64_t& blocks, hipStream_t s) {
   if (a.count == 0) return MAO_OK;

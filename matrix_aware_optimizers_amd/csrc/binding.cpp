@@ -406,6 +406,91 @@ PyObject* linear_backward_weight(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// One token per row.
+const int64_t* tokens_of(PyObject* o, int64_t rows, int64_t dev) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor& t = tensor(o);
+  if (t.scalar_type() != at::kLong) fail(PyExc_TypeError, "targets must be int64");
+  if (t.dim() != 1 || t.size(0) != rows || !t.is_contiguous())
+    fail(PyExc_ValueError, "targets must be a contiguous vector with one token per row");
+  on_device(t, dev);
+  return (const int64_t*)t.data_ptr();
+}
+
+// (X, targets, entropy, top, device, stream)
+// -> (logprob, entropy, stats, top_logprobs, top_ids), None for what is not asked for
+PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 6, [&]() -> PyObject* {
+    const int64_t dev = integer(a[4]), stream = integer(a[5]), top = integer(a[3]);
+    const at::Tensor& X = tensor(a[0]);
+    const mao_mat x = view(X, dev);
+    const int64_t* targets = tokens_of(a[1], x.rows, dev);
+    if (top < 0 || top > INT32_MAX) fail(PyExc_ValueError, "top must not be negative");
+    const auto f = X.options().dtype(at::kFloat);
+    at::Tensor lp, ent, top_lp, ids;
+    if (targets) lp = at::empty({x.rows}, f);
+    if (a[2] == Py_True) ent = at::empty({x.rows}, f);
+    const at::Tensor stats = at::empty({x.rows, 2}, f);
+    // a top that the call refuses allocates nothing
+    const int64_t k = top <= x.cols && top <= 32 ? top : 0;
+    if (k) {
+      top_lp = at::empty({x.rows, k}, f);
+      ids = at::empty({x.rows, k}, X.options().dtype(at::kLong));
+    }
+    const Workspace ws(mao_token_logprobs_workspace_size(x.rows, x.cols, (int32_t)top), dev, stream);
+    check(mao_token_logprobs(x, targets, targets ? (float*)lp.data_ptr() : nullptr,
+                             ent.defined() ? (float*)ent.data_ptr() : nullptr,
+                             (float*)stats.data_ptr(), (int32_t)top,
+                             k ? (float*)top_lp.data_ptr() : nullptr,
+                             k ? (int64_t*)ids.data_ptr() : nullptr, ws.p, ws.bytes, (void*)stream),
+          "mao_token_logprobs");
+    const auto out = [](const at::Tensor& t) {
+      return t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None);
+    };
+    return Py_BuildValue("NNNNN", out(lp), out(ent), out(stats), out(top_lp), out(ids));
+  });
+}
+
+// (X, targets, stats, entropy, dlogprob, dentropy, dlse, out, device, stream) -> dX
+PyObject* token_logprobs_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 10, [&]() -> PyObject* {
+    const int64_t dev = integer(a[8]), stream = integer(a[9]);
+    const at::Tensor& X = tensor(a[0]);
+    const mao_mat x = view(X, dev);
+    const int64_t* targets = tokens_of(a[1], x.rows, dev);
+    const at::Tensor& st = tensor(a[2]);
+    if (st.scalar_type() != at::kFloat) fail(PyExc_TypeError, "stats must be float32");
+    if (st.dim() != 2 || st.size(0) != x.rows || st.size(1) != 2 || !st.is_contiguous())
+      fail(PyExc_ValueError, "stats must be the forward pass's (rows x 2)");
+    on_device(st, dev);
+    const Vec ent(a[3], x.rows, dev, "entropy", true), dlp(a[4], x.rows, dev, "dlogprob", true),
+        de(a[5], x.rows, dev, "dentropy", true), dl(a[6], x.rows, dev, "dlse", true);
+    const at::Tensor out = result(a[7], x.rows, x.cols, X.scalar_type(), X);
+    check(mao_token_logprobs_backward(x, targets, (const float*)st.data_ptr(), (const float*)ent.p,
+                                      (const float*)dlp.p, (const float*)de.p, (const float*)dl.p,
+                                      view(out, dev), (void*)stream),
+          "mao_token_logprobs_backward");
+    return wrap(out, a[7]);
+  });
+}
+
+// (X, targets, weight, out, device, stream) -> (logprob, dX)
+PyObject* token_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 6, [&]() -> PyObject* {
+    const int64_t dev = integer(a[4]), stream = integer(a[5]);
+    const at::Tensor& X = tensor(a[0]);
+    const mao_mat x = view(X, dev);
+    const int64_t* targets = tokens_of(a[1], x.rows, dev);
+    const Vec w(a[2], x.rows, dev, "weight", true);
+    const at::Tensor lp = at::empty({x.rows}, X.options().dtype(at::kFloat));
+    const at::Tensor out = result(a[3], x.rows, x.cols, X.scalar_type(), X);
+    check(mao_token_loss(x, targets, (const float*)w.p, (float*)lp.data_ptr(), view(out, dev),
+                         (void*)stream),
+          "mao_token_loss");
+    return Py_BuildValue("NN", THPVariable_Wrap(lp), wrap(out, a[3]));
+  });
+}
+
 // The elements of a tensor that an optimizer step reads or writes in place (autograd looks on
 // at none of it, as with the other steps).
 struct Flat {
@@ -589,6 +674,9 @@ PyMethodDef g_methods[] = {MAO_METHOD(init),
                            MAO_METHOD(linear),
                            MAO_METHOD(linear_backward_input),
                            MAO_METHOD(linear_backward_weight),
+                           MAO_METHOD(token_logprobs),
+                           MAO_METHOD(token_logprobs_backward),
+                           MAO_METHOD(token_loss),
                            MAO_METHOD(adamw_step_many),
                            MAO_METHOD(adamw8_read),
                            {nullptr, nullptr, 0, nullptr}};

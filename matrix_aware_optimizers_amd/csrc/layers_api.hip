@@ -110,6 +110,28 @@ WeightWs carve_weight(void* base, int64_t rows, int64_t k, int64_t n, int dtype,
   return w;
 }
 
+// The parts of a row's work: sums, then alternatives.
+struct TokenWs {
+  float* sums;
+  uint64_t* keys;
+  size_t bytes;
+};
+TokenWs carve_tokens(void* base, int64_t rows, int64_t vocab, int top) {
+  const TokenCut cut = token_cut(rows, vocab);
+  Carver c(base);
+  TokenWs w = {};
+  if (cut.parts == 1) return w;
+  w.sums = c.take<float>((size_t)rows * cut.parts * 4);
+  if (top) w.keys = c.take<uint64_t>((size_t)rows * cut.parts * top);
+  w.bytes = c.used;
+  return w;
+}
+
+mao_status check_targets(const int64_t* t) {
+  if ((uintptr_t)t % 8 != 0) MAO_FAIL(MAO_E_LAYOUT, "targets misaligned");
+  return MAO_OK;
+}
+
 }  // namespace
 }  // namespace mao
 
@@ -468,6 +490,131 @@ mao_status mao_linear_backward_weight(mao_mat dY, const mao_mat* X, const mao_q8
     MAO_TRY(launch_partial_sum(w.sums, p.M, lin_sum_rows(dY.dtype, p.M, p.N, p.K), p.M, dbias,
                                nullptr, 0, accumulate != 0, s));
   return MAO_OK;
+}
+
+size_t mao_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int32_t top) {
+  if (!sizes_ok(rows, vocab, 1) || top < 0 || top > kTokenTop || top > vocab) return 0;
+  return carve_tokens(nullptr, rows, vocab, top).bytes;
+}
+
+mao_status mao_token_logprobs(mao_mat X, const int64_t* targets, float* logprob, float* entropy,
+                              float* stats, int32_t top, float* top_logprobs, int64_t* top_ids,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  MAO_TRY(check_view("X", X));
+  if ((targets != nullptr) != (logprob != nullptr)) MAO_FAIL(MAO_E_NULL, "targets and logprob go together");
+  if (top < 0 || top > kTokenTop || top > X.cols)
+    MAO_FAIL(MAO_E_HPARAM, "top=%d outside 0..min(%d, vocabulary)", top, kTokenTop);
+  if ((top != 0) != (top_logprobs != nullptr) || (top != 0) != (top_ids != nullptr))
+    MAO_FAIL(MAO_E_NULL, "top_logprobs and top_ids go with top > 0");
+  if (!logprob && !entropy && !stats && !top) MAO_FAIL(MAO_E_NULL, "no result is asked for");
+  MAO_TRY(check_targets(targets));
+  MAO_TRY(check_floats("logprob", logprob));
+  MAO_TRY(check_floats("entropy", entropy));
+  MAO_TRY(check_floats("stats", stats));
+  MAO_TRY(check_floats("top_logprobs", top_logprobs));
+  if ((uintptr_t)top_ids % 8 != 0) MAO_FAIL(MAO_E_LAYOUT, "top_ids misaligned");
+  const TokenWs w = carve_tokens(workspace, X.rows, X.cols, top);
+  MAO_TRY(check_workspace(workspace, workspace_bytes, w.bytes));
+  Buffers b;
+  if (logprob) b.out(range_of(logprob, X.rows * 4));
+  if (entropy) b.out(range_of(entropy, X.rows * 4));
+  if (stats) b.out(range_of(stats, X.rows * 8));
+  if (top) b.out(range_of(top_logprobs, X.rows * top * 4));
+  if (top) b.out(range_of(top_ids, X.rows * top * 8));
+  if (w.bytes) b.out(range_of(workspace, (int64_t)w.bytes));
+  b.in(range_of(X));
+  if (targets) b.in(range_of(targets, X.rows * 8));
+  MAO_TRY(b.check());
+  const TokenCut cut = token_cut(X.rows, X.cols);
+  TokenArgs a = {};
+  a.x = X.data;
+  a.ldx = X.ld;
+  a.rows = (int)X.rows;
+  a.vocab = (int)X.cols;
+  a.targets = targets;
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.stats = stats;
+  a.top = top;
+  a.top_logprobs = top_logprobs;
+  a.top_ids = top_ids;
+  a.parts = cut.parts;
+  a.part_runs = cut.part_runs;
+  a.part_sums = w.sums;
+  a.part_keys = w.keys;
+  return launch_tokens(a, X.dtype, (hipStream_t)stream);
+}
+
+mao_status mao_token_logprobs_backward(mao_mat X, const int64_t* targets, const float* stats,
+                                       const float* entropy, const float* dlogprob,
+                                       const float* dentropy, const float* dlse, mao_mat dX,
+                                       void* stream) {
+  MAO_TRY(check_view("X", X));
+  MAO_TRY(check_shape("dX", dX, X.rows, X.cols));
+  if (!stats) MAO_FAIL(MAO_E_NULL, "stats is NULL");
+  if (!dlogprob && !dentropy && !dlse) MAO_FAIL(MAO_E_NULL, "no gradient is given");
+  if (dlogprob && !targets) MAO_FAIL(MAO_E_NULL, "dlogprob needs targets");
+  if (dentropy && !entropy) MAO_FAIL(MAO_E_NULL, "dentropy needs entropy");
+  MAO_TRY(check_targets(targets));
+  MAO_TRY(check_floats("stats", stats));
+  MAO_TRY(check_floats("entropy", entropy));
+  MAO_TRY(check_floats("dlogprob", dlogprob));
+  MAO_TRY(check_floats("dentropy", dentropy));
+  MAO_TRY(check_floats("dlse", dlse));
+  Buffers b;
+  b.out(range_of(dX));
+  if (!same_view(X, dX)) b.in(range_of(X));
+  if (targets) b.in(range_of(targets, X.rows * 8));
+  b.in(range_of(stats, X.rows * 8));
+  if (entropy) b.in(range_of(entropy, X.rows * 4));
+  if (dlogprob) b.in(range_of(dlogprob, X.rows * 4));
+  if (dentropy) b.in(range_of(dentropy, X.rows * 4));
+  if (dlse) b.in(range_of(dlse, X.rows * 4));
+  MAO_TRY(b.check());
+  TokenBackArgs a = {};
+  a.x = X.data;
+  a.ldx = X.ld;
+  a.rows = (int)X.rows;
+  a.vocab = (int)X.cols;
+  a.targets = targets;
+  a.stats = stats;
+  a.entropy = entropy;
+  a.dlogprob = dlogprob;
+  a.dentropy = dentropy;
+  a.dlse = dlse;
+  a.dx = dX.data;
+  a.lddx = dX.ld;
+  a.dx_dtype = dX.dtype;
+  return launch_tokens_backward(a, X.dtype, (hipStream_t)stream);
+}
+
+mao_status mao_token_loss(mao_mat X, const int64_t* targets, const float* weight, float* logprob,
+                          mao_mat dX, void* stream) {
+  MAO_TRY(check_view("X", X));
+  MAO_TRY(check_shape("dX", dX, X.rows, X.cols));
+  if (!targets) MAO_FAIL(MAO_E_NULL, "targets is NULL");
+  MAO_TRY(check_targets(targets));
+  MAO_TRY(check_floats("weight", weight));
+  MAO_TRY(check_floats("logprob", logprob));
+  Buffers b;
+  b.out(range_of(dX));
+  if (logprob) b.out(range_of(logprob, X.rows * 4));
+  if (!same_view(X, dX)) b.in(range_of(X));
+  b.in(range_of(targets, X.rows * 8));
+  if (weight) b.in(range_of(weight, X.rows * 4));
+  MAO_TRY(b.check());
+  TokenBackArgs a = {};
+  a.x = X.data;
+  a.ldx = X.ld;
+  a.rows = (int)X.rows;
+  a.vocab = (int)X.cols;
+  a.targets = targets;
+  a.weight = weight;
+  a.logprob = logprob;
+  a.dx = dX.data;
+  a.lddx = dX.ld;
+  a.dx_dtype = dX.dtype;
+  return launch_token_loss(a, X.dtype, (hipStream_t)stream);
 }
 
 }  // extern "C"
