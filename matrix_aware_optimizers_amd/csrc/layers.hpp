@@ -221,9 +221,9 @@ struct TokenBackArgs {
   void* dx;                                 // may be x
   int64_t ldx, lddx;
   int rows, vocab, dx_dtype;
-  int parts, part_runs;
+  int parts, part_runs;  // set by the launch
 };
-mao_status launch_tokens_backward(TokenBackArgs a, int dtype, hipStream_t s);
+mao_status launch_tokens_backward(const TokenBackArgs& a, int dtype, hipStream_t s);
 mao_status launch_token_loss(const TokenBackArgs& a, int dtype, hipStream_t s);
 
 }  // namespace mao

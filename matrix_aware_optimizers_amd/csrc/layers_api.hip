@@ -127,6 +127,8 @@ TokenWs carve_tokens(void* base, int64_t rows, int64_t vocab, int top) {
   return w;
 }
 
+constexpr int64_t kMostBlocks = (1 << 24) - 1;  // of 256 threads: a launch has below 2^32
+
 mao_status check_targets(const int64_t* t) {
   if ((uintptr_t)t % 8 != 0) MAO_FAIL(MAO_E_LAYOUT, "targets misaligned");
   return MAO_OK;
@@ -561,6 +563,7 @@ mao_status mao_token_logprobs_backward(mao_mat X, const int64_t* targets, const 
   MAO_TRY(check_floats("dlogprob", dlogprob));
   MAO_TRY(check_floats("dentropy", dentropy));
   MAO_TRY(check_floats("dlse", dlse));
+  if (X.rows * ceil_div(X.cols, 8192) > kMostBlocks) MAO_FAIL(MAO_E_UNSUPPORTED, "more than 2^32 threads");
   Buffers b;
   b.out(range_of(dX));
   if (!same_view(X, dX)) b.in(range_of(X));

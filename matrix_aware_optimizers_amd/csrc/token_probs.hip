@@ -84,7 +84,7 @@ __device__ __forceinline__ void add_runs(Sums& q, const float (&v)[R][8]) {
   if (ENT) q.t += (t[0] + t[1]) + (t[2] + t[3]);
 }
 
-// Sums over the block's threads, in every thread. buf: 3 floats per wavefront.
+// Sums over the block's threads, in every thread. buf: 3 floats per wavefront, used once.
 template <int THREADS>
 __device__ __forceinline__ Sums block_sums(Sums q, float (*buf)[3]) {
   const float m = wave_max(q.m);
@@ -94,7 +94,6 @@ __device__ __forceinline__ Sums block_sums(Sums q, float (*buf)[3]) {
   if constexpr (THREADS > 64) {
     constexpr int NW = THREADS / 64;
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    __syncthreads();
     if (lane == 0) {
       buf[w][0] = q.m;
       buf[w][1] = q.s;
@@ -139,49 +138,58 @@ struct TopShared {
   uint32_t count, limit, need;
 };
 
-// The `top` largest keys of the runs [lo, hi) of a row into sh.list[0 .. top), in order; m:
-// the largest logit of this thread's runs. Keys past the part's elements are 0.
+// The `top` largest keys of the runs [lo, hi) of a row, each handed to emit with its place
+// in the order; places past the part's elements get key 0. m: the largest logit of this
+// thread's runs, which `kept` holds if KEEP (one block of R a thread).
 //
-// The threads form 64 groups; the top-th largest of the groups' maxima is a limit that at
-// least `top` logits reach and, of logits in no order, few more do. Threads whose own
-// maximum reaches it look through their runs again (read a moment before). Where too
-// many reach it (ties; a mask that leaves a few neighbours), the exact limit is found by four
-// histograms of 8 bits each, and of the logits equal to it the lowest tokens are taken.
-template <typename T, int THREADS>
-__device__ void select_top(const T* x, int vocab, int lo, int hi, int top, float m, TopShared& sh) {
+// The threads form 64 groups; the top-th largest of the groups' maxima (its upper 16 bits)
+// is a limit that at least `top` logits reach and, of logits in no order, few more do. Threads
+// whose own maximum reaches it look through their runs. Where too many reach it (ties; a
+// mask that leaves a few neighbours), the exact limit is found by four histograms of 8
+// bits each, and of the logits equal to it the lowest tokens are taken.
+template <int THREADS>
+__device__ __forceinline__ void group_maxima(float m, bool any, TopShared& sh) {
+  constexpr int GROUP = THREADS / 64;
+  uint32_t g = any ? ordered(m) : 0;
+#pragma unroll
+  for (int off = 1; off < GROUP; off <<= 1) g = max(g, (uint32_t)__shfl_xor((int)g, off, 64));
+  if ((threadIdx.x & (GROUP - 1)) == 0) sh.group[threadIdx.x / GROUP] = g;
+  if (threadIdx.x == 0) sh.count = 0;
+}
+
+// After group_maxima and a barrier.
+template <typename T, int THREADS, bool KEEP, int R, typename Emit>
+__device__ __forceinline__ void select_top(const T* x, int vocab, int lo, int hi, int top, float m,
+                                           const float (&kept)[R][8], TopShared& sh, Emit emit) {
   const int tid = threadIdx.x;
-  if (m == kNone) m = -INFINITY;  // none but masked logits, perhaps
+  uint32_t limit = 0;
   {
-    uint32_t g = ordered(m);
-    if (lo + tid >= hi) g = 0;  // no run at all
-    constexpr int GROUP = THREADS / 64;
+    const uint32_t g = sh.group[tid & 63];
 #pragma unroll
-    for (int off = 1; off < GROUP; off <<= 1) g = max(g, (uint32_t)__shfl_xor((int)g, off, 64));
-    if ((tid & (GROUP - 1)) == 0) sh.group[tid / GROUP] = g;
-    if (tid == 0) sh.count = 0;
-  }
-  __syncthreads();
-  if (tid < 64) {
-    const uint32_t g = sh.group[tid];
-    int rank = 0;
-    for (int j = 0; j < 64; ++j) {
-      const uint32_t o = sh.group[j];
-      rank += o > g || (o == g && j < tid);
+    for (int bit = 31; bit >= 16; --bit) {
+      const uint32_t higher = limit | 1u << bit;
+      if (__popcll(__ballot(g >= higher)) >= top) limit = higher;
     }
-    if (rank == top - 1) sh.limit = g;
   }
-  __syncthreads();
-  const uint32_t limit = sh.limit;
-  if (lo + tid < hi && ordered(m) >= limit) {
-    for (int run = lo + tid; run < hi; run += THREADS) {
-      float v[8];
-      load_logits(x, run, vocab, v);
+  auto offer = [&](const float (&v)[8], int run) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (8 * run + i < vocab && ordered(v[i]) >= limit) {
-          const uint32_t at = atomicAdd(&sh.count, 1u);
-          if (at < kList) sh.list[at] = key_of(v[i], 8 * run + i);
-        }
+    for (int i = 0; i < 8; ++i) {
+      if (8 * run + i < vocab && ordered(v[i]) >= limit) {
+        const uint32_t at = atomicAdd(&sh.count, 1u);
+        if (at < kList) sh.list[at] = key_of(v[i], 8 * run + i);
+      }
+    }
+  };
+  if (lo + tid < hi && ordered(m) >= limit) {
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (lo + tid + r * THREADS < hi) offer(kept[r], lo + tid + r * THREADS);
+    } else {
+      for (int run = lo + tid; run < hi; run += THREADS) {
+        float v[8];
+        load_logits(x, run, vocab, v);
+        offer(v, run);
       }
     }
   }
@@ -269,28 +277,16 @@ __device__ void select_top(const T* x, int vocab, int lo, int hi, int top, float
     if (tid == 0) sh.count = (uint32_t)top;
     __syncthreads();
   }
-  // sorted by counting the larger ones (keys are distinct); the list holds at least
-  // min(top, elements) keys
+  // in order by counting the larger ones: keys are distinct, and at least min(top, elements)
   const int n = (int)sh.count;
-  uint64_t mine[kList / THREADS > 0 ? kList / THREADS : 1];
-  int rank[kList / THREADS > 0 ? kList / THREADS : 1];
-#pragma unroll
-  for (int k = 0; k < (int)(sizeof(rank) / sizeof(rank[0])); ++k) {
-    const int c = tid + k * THREADS;
-    rank[k] = kList;
-    if (c < n) {
-      mine[k] = sh.list[c];
-      int r = 0;
-      for (int j = 0; j < n; ++j) r += sh.list[j] > mine[k];
-      rank[k] = r;
-    }
+  for (int c = tid; c < n; c += THREADS) {
+    const uint64_t mine = sh.list[c];
+    int rank = 0;
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) rank += sh.list[j] > mine;
+    if (rank < top) emit(rank, mine);
   }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < (int)(sizeof(rank) / sizeof(rank[0])); ++k)
-    if (rank[k] < top) sh.list[rank[k]] = mine[k];
-  for (int k = n + tid; k < top; k += THREADS) sh.list[k] = 0;
-  __syncthreads();
+  for (int k = n + tid; k < top; k += THREADS) emit(k, 0);
 }
 
 // What a row's sums give.
@@ -328,8 +324,8 @@ __device__ __forceinline__ void write_top(const TokenArgs& a, int64_t row, const
 }
 
 // One workgroup per part of a row; parts == 1: the row's results, else the part's sums
-// (a.part_sums) and alternatives (a.part_keys).
-template <typename T, int THREADS, bool ENT, bool TOP>
+// (a.part_sums) and alternatives (a.part_keys). KEEP: the part is one block of R runs a thread.
+template <typename T, int THREADS, bool ENT, bool TOP, bool KEEP>
 __global__ __launch_bounds__(THREADS) void token_kernel(TokenArgs a) {
   constexpr int R = 4;
   __shared__ float buf[THREADS / 64][3];
@@ -340,13 +336,14 @@ __global__ __launch_bounds__(THREADS) void token_kernel(TokenArgs a) {
   const int lo = part * a.part_runs, hi = min(runs, lo + a.part_runs);
   Sums q;
   q.init();
-  for (int base = lo + (int)threadIdx.x; base < hi; base += R * THREADS) {
-    float v[R][8];
+  float v[R][8];
+  int base = lo + (int)threadIdx.x;
+  do {
     Raw8<T> raw[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int run = base + r * THREADS;
-      // past the end: the row's first run once more, replaced below
+      // past the end: the part's first run once more, replaced below
       raw[r].load_cut(x + 8 * (int64_t)(run < hi ? run : lo), run < hi ? a.vocab - 8 * run : 8);
     }
 #pragma unroll
@@ -357,18 +354,31 @@ __global__ __launch_bounds__(THREADS) void token_kernel(TokenArgs a) {
       if (valid < 8) cut_run(v[r], valid);
     }
     add_runs<ENT, R>(q, v);
-  }
-  const float mine = q.m;
-  q = block_sums<THREADS>(q, buf);
+    base += R * THREADS;
+  } while (!KEEP && base < hi);
   if constexpr (TOP) {
     __shared__ TopShared sh;
-    if (q.s == q.s) select_top<T, THREADS>(x, a.vocab, lo, hi, a.top, mine, sh);
+    // kNone: masked logits alone, or none that is larger than the lowest number
+    const float mine = q.m == kNone ? -INFINITY : q.m;
+    group_maxima<THREADS>(mine, lo + (int)threadIdx.x < hi, sh);
+    if constexpr (THREADS == 64) __syncthreads();
+    q = block_sums<THREADS>(q, buf);
     if (a.parts == 1) {
-      for (int k = threadIdx.x; k < a.top; k += THREADS) write_top(a, row, q, k, sh.list[k]);
+      auto out = [&](int k, uint64_t key) { write_top(a, row, q, k, key); };
+      if (q.s == q.s)
+        select_top<T, THREADS, KEEP, R>(x, a.vocab, lo, hi, a.top, mine, v, sh, out);
+      else
+        for (int k = threadIdx.x; k < a.top; k += THREADS) out(k, 0);
     } else {
-      for (int k = threadIdx.x; k < a.top; k += THREADS)
-        a.part_keys[(int64_t)blockIdx.x * a.top + k] = q.s == q.s ? sh.list[k] : 0;
+      uint64_t* keys = a.part_keys + (int64_t)blockIdx.x * a.top;
+      auto out = [&](int k, uint64_t key) { keys[k] = key; };
+      if (q.s == q.s)
+        select_top<T, THREADS, KEEP, R>(x, a.vocab, lo, hi, a.top, mine, v, sh, out);
+      else
+        for (int k = threadIdx.x; k < a.top; k += THREADS) out(k, 0);
     }
+  } else {
+    q = block_sums<THREADS>(q, buf);
   }
   if (threadIdx.x != 0) return;
   if (a.parts == 1) {
@@ -381,12 +391,11 @@ __global__ __launch_bounds__(THREADS) void token_kernel(TokenArgs a) {
   }
 }
 
-// The join of a row's parts: one wavefront per row.
-template <typename T>
-__global__ __launch_bounds__(64) void token_join_kernel(TokenArgs a) {
-  __shared__ uint64_t keys[kTokenParts * kTokenTop];
+// The join of a row's parts: one workgroup per row, of one wavefront without alternatives.
+template <typename T, bool TOP>
+__global__ __launch_bounds__(TOP ? 256 : 64) void token_join_kernel(TokenArgs a) {
   const int64_t row = blockIdx.x;
-  const int lane = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63;
   Sums q;
   q.init();
   if (lane < a.parts) {
@@ -395,29 +404,35 @@ __global__ __launch_bounds__(64) void token_join_kernel(TokenArgs a) {
     q.s = p[1];
     q.t = p[2];
   }
-  q.raise(wave_max(q.m));
-  q.s = wave_total(q.s);
-  q.t = wave_total(q.t);
-  if (a.top) {
+  if constexpr (TOP) {
+    constexpr int kMost = kTokenParts * kTokenTop;
+    __shared__ uint64_t keys[kMost];
     const int n = a.parts * a.top;
-    const uint64_t* from = a.part_keys + row * n;
-    for (int k = lane; k < n; k += 64) keys[k] = from[k];
+    for (int k = tid; k < n; k += 256) keys[k] = a.part_keys[row * n + k];
+    q.raise(wave_max(q.m));
+    q.s = wave_total(q.s);
+    q.t = wave_total(q.t);
     __syncthreads();
-    for (int k = lane; k < n; k += 64) {
+    for (int k = tid; k < n; k += 256) {
       const uint64_t mine = keys[k];
       if (mine == 0 && q.s == q.s) continue;  // no element
       int rank = 0;
       // equal ones only in a row with a NaN, whose parts have none
+#pragma unroll 8
       for (int j = 0; j < n; ++j) rank += keys[j] > mine || (keys[j] == mine && j < k);
       if (rank < a.top) write_top(a, row, q, rank, mine);
     }
+  } else {
+    q.raise(wave_max(q.m));
+    q.s = wave_total(q.s);
+    q.t = wave_total(q.t);
   }
-  if (lane == 0) write_row<T>(a, row, q);
+  if (tid == 0) write_row<T>(a, row, q);
 }
 
 // The gradient, a segment of a row per workgroup. ENT: the entropy's too.
-template <typename T, typename TO, bool ENT>
-__global__ __launch_bounds__(256) void token_backward_kernel(TokenBackArgs a) {
+template <typename T, typename TO, int THREADS, bool ENT>
+__global__ __launch_bounds__(THREADS) void token_backward_kernel(TokenBackArgs a) {
   const int64_t row = blockIdx.x / a.parts;
   const int part = (int)(blockIdx.x - row * a.parts);
   const int runs = (a.vocab + 7) >> 3;
@@ -432,15 +447,30 @@ __global__ __launch_bounds__(256) void token_backward_kernel(TokenBackArgs a) {
   const bool empty = m == -INFINITY;
   if (empty) dlp = 0.f;
   const bool nothing = empty || (dl == 0.f && de == 0.f);
-  for (int run = lo + (int)threadIdx.x; run < hi; run += blockDim.x) {
-    float v[8], o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (!nothing) {  // else the row may hold anything
-      load_logits(x, run, a.vocab, v);
+  constexpr int R = 4;  // a segment is one block of runs
+  Raw8<T> raw[R];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float y = (v[i] - m) - log_s, p = exp_hw(y);
-        o[i] = p * (ENT ? dl - de * (fmaxf(y, -1e4f) + h) : dl);
-      }
+  for (int r = 0; r < R; ++r) {
+    const int run = lo + (int)threadIdx.x + r * THREADS;
+    if (nothing || run >= hi)  // nothing: the row may hold anything
+      raw[r].zero();
+    else
+      raw[r].load_cut(x + 8 * (int64_t)run, a.vocab - 8 * run);
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int run = lo + (int)threadIdx.x + r * THREADS;
+    if (run >= hi) break;
+    float v[8], o[8];
+    raw[r].get(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y = (v[i] - m) - log_s, p = exp_hw(y);
+      o[i] = p * (ENT ? dl - de * (fmaxf(y, -1e4f) + h) : dl);
+    }
+    if (nothing) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = 0.f;
     }
     const int64_t at = target - 8 * (int64_t)run;
     if (at >= 0 && at < 8) {
@@ -552,41 +582,51 @@ __global__ __launch_bounds__(THREADS) void token_loss_kernel(TokenBackArgs a) {
   }
 }
 
-template <typename T, int THREADS>
+template <typename T, int THREADS, bool KEEP>
 mao_status forward_go(const TokenArgs& a, hipStream_t s) {
   const dim3 grid((uint32_t)((int64_t)a.rows * a.parts));
   const bool ent = a.entropy != nullptr, top = a.top != 0;
-#define MAO_TOKEN(E, P) hipLaunchKernelGGL((token_kernel<T, THREADS, E, P>), grid, dim3(THREADS), 0, s, a)
+#define MAO_TOKEN(E, P) \
+  hipLaunchKernelGGL((token_kernel<T, THREADS, E, P, KEEP>), grid, dim3(THREADS), 0, s, a)
   if (ent && top) MAO_TOKEN(true, true);
   else if (ent) MAO_TOKEN(true, false);
   else if (top) MAO_TOKEN(false, true);
   else MAO_TOKEN(false, false);
 #undef MAO_TOKEN
   MAO_LAUNCH_CHECK();
-  if (a.parts > 1) {
-    hipLaunchKernelGGL((token_join_kernel<T>), dim3(a.rows), dim3(64), 0, s, a);
-    MAO_LAUNCH_CHECK();
-  }
+  if (a.parts == 1) return MAO_OK;
+  if (top)
+    hipLaunchKernelGGL((token_join_kernel<T, true>), dim3(a.rows), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((token_join_kernel<T, false>), dim3(a.rows), dim3(64), 0, s, a);
+  MAO_LAUNCH_CHECK();
   return MAO_OK;
 }
 
 template <typename T>
 mao_status forward_pick(const TokenArgs& a, hipStream_t s) {
-  const int runs = a.part_runs;
-  if (runs <= 128) return forward_go<T, 64>(a, s);
-  if (runs <= 1024) return forward_go<T, 256>(a, s);
-  return forward_go<T, 1024>(a, s);
+  if (a.part_runs <= 64 * 4) return forward_go<T, 64, true>(a, s);
+  if (a.part_runs <= 256 * 4) return forward_go<T, 256, true>(a, s);
+  return forward_go<T, 256, false>(a, s);
+}
+
+template <typename T, typename TO, int THREADS>
+mao_status backward_go(TokenBackArgs a, hipStream_t s) {
+  const int64_t runs = ceil_div(a.vocab, 8);
+  a.parts = (int)ceil_div(runs, 4 * THREADS);
+  a.part_runs = (int)ceil_div(runs, a.parts);
+  const dim3 grid((uint32_t)((int64_t)a.rows * a.parts));
+  if (a.dentropy)
+    hipLaunchKernelGGL((token_backward_kernel<T, TO, THREADS, true>), grid, dim3(THREADS), 0, s, a);
+  else
+    hipLaunchKernelGGL((token_backward_kernel<T, TO, THREADS, false>), grid, dim3(THREADS), 0, s, a);
+  MAO_LAUNCH_CHECK();
+  return MAO_OK;
 }
 
 template <typename T, typename TO>
-mao_status backward_go(const TokenBackArgs& a, int threads, hipStream_t s) {
-  const dim3 grid((uint32_t)((int64_t)a.rows * a.parts));
-  if (a.dentropy)
-    hipLaunchKernelGGL((token_backward_kernel<T, TO, true>), grid, dim3(threads), 0, s, a);
-  else
-    hipLaunchKernelGGL((token_backward_kernel<T, TO, false>), grid, dim3(threads), 0, s, a);
-  MAO_LAUNCH_CHECK();
-  return MAO_OK;
+mao_status backward_pick(const TokenBackArgs& a, hipStream_t s) {
+  return a.vocab <= 64 * 4 * 8 ? backward_go<T, TO, 64>(a, s) : backward_go<T, TO, 256>(a, s);
 }
 
 template <typename T, int THREADS, int R, bool KEEP>
@@ -610,10 +650,10 @@ mao_status loss_pick(const TokenBackArgs& a, hipStream_t s) {
 }  // namespace
 
 TokenCut token_cut(int64_t rows, int64_t vocab) {
-  // at least two workgroups per CU, of at least 1024 runs of 8 each
+  // six workgroups per CU, of at least one block of 1024 runs of 8 each
   const int64_t runs = ceil_div(vocab, 8);
-  int64_t parts = std::min<int64_t>(kTokenParts, ceil_div(512, rows));
-  parts = std::max<int64_t>(1, std::min(parts, runs / 1024));
+  int64_t parts = std::min<int64_t>(kTokenParts, ceil_div(6 * 256, rows));
+  parts = std::max<int64_t>(1, std::min(parts, ceil_div(runs, 1024)));
   const int64_t per = ceil_div(runs, parts);
   return {(int)ceil_div(runs, per), (int)per};
 }
@@ -622,17 +662,12 @@ mao_status launch_tokens(const TokenArgs& a, int dtype, hipStream_t s) {
   return dtype == MAO_BF16 ? forward_pick<bf16_t>(a, s) : forward_pick<float>(a, s);
 }
 
-mao_status launch_tokens_backward(TokenBackArgs a, int dtype, hipStream_t s) {
-  // segments of up to 1024 runs of 8
-  const int64_t runs = ceil_div(a.vocab, 8);
-  a.parts = (int)ceil_div(runs, 1024);
-  a.part_runs = (int)ceil_div(runs, a.parts);
-  const int threads = runs <= 64 ? 64 : 256;
+mao_status launch_tokens_backward(const TokenBackArgs& a, int dtype, hipStream_t s) {
   if (dtype == MAO_BF16)
-    return a.dx_dtype == MAO_BF16 ? backward_go<bf16_t, bf16_t>(a, threads, s)
-                                  : backward_go<bf16_t, float>(a, threads, s);
-  return a.dx_dtype == MAO_BF16 ? backward_go<float, bf16_t>(a, threads, s)
-                                : backward_go<float, float>(a, threads, s);
+    return a.dx_dtype == MAO_BF16 ? backward_pick<bf16_t, bf16_t>(a, s)
+                                  : backward_pick<bf16_t, float>(a, s);
+  return a.dx_dtype == MAO_BF16 ? backward_pick<float, bf16_t>(a, s)
+                                : backward_pick<float, float>(a, s);
 }
 
 mao_status launch_token_loss(const TokenBackArgs& a, int dtype, hipStream_t s) {
