@@ -329,8 +329,9 @@ template <typename T, int THREADS, bool ENT, bool TOP, bool KEEP>
 __global__ __launch_bounds__(THREADS) void token_kernel(TokenArgs a) {
   constexpr int R = 4;
   __shared__ float buf[THREADS / 64][3];
-  const int64_t row = blockIdx.x / a.parts;
-  const int part = (int)(blockIdx.x - row * a.parts);
+  const uint32_t line = blockIdx.x / (uint32_t)a.parts;
+  const int64_t row = line;
+  const int part = (int)(blockIdx.x - line * (uint32_t)a.parts);
   const T* x = (const T*)a.x + row * a.ldx;
   const int runs = (a.vocab + 7) >> 3;
   const int lo = part * a.part_runs, hi = min(runs, lo + a.part_runs);
@@ -433,11 +434,19 @@ __global__ __launch_bounds__(TOP ? 256 : 64) void token_join_kernel(TokenArgs a)
 // The gradient, a segment of a row per workgroup. ENT: the entropy's too.
 template <typename T, typename TO, int THREADS, bool ENT>
 __global__ __launch_bounds__(THREADS) void token_backward_kernel(TokenBackArgs a) {
-  const int64_t row = blockIdx.x / a.parts;
-  const int part = (int)(blockIdx.x - row * a.parts);
+  const uint32_t line = blockIdx.x / (uint32_t)a.parts;
+  const int64_t row = line;
+  const int part = (int)(blockIdx.x - line * (uint32_t)a.parts);
   const int runs = (a.vocab + 7) >> 3;
   const int lo = part * a.part_runs, hi = min(runs, lo + a.part_runs);
   const T* x = (const T*)a.x + row * a.ldx;
+  constexpr int R = 4;  // a segment is one block of runs
+  Raw8<T> raw[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int run = lo + (int)threadIdx.x + r * THREADS;
+    if (run < hi) raw[r].load_cut(x + 8 * (int64_t)run, a.vocab - 8 * run);
+  }
   const int64_t target = a.targets ? a.targets[row] : -1;
   const float m = a.stats[2 * row], log_s = a.stats[2 * row + 1];
   float dlp = a.dlogprob && target >= 0 ? a.dlogprob[row] : 0.f;
@@ -447,16 +456,6 @@ __global__ __launch_bounds__(THREADS) void token_backward_kernel(TokenBackArgs a
   const bool empty = m == -INFINITY;
   if (empty) dlp = 0.f;
   const bool nothing = empty || (dl == 0.f && de == 0.f);
-  constexpr int R = 4;  // a segment is one block of runs
-  Raw8<T> raw[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int run = lo + (int)threadIdx.x + r * THREADS;
-    if (nothing || run >= hi)  // nothing: the row may hold anything
-      raw[r].zero();
-    else
-      raw[r].load_cut(x + 8 * (int64_t)run, a.vocab - 8 * run);
-  }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int run = lo + (int)threadIdx.x + r * THREADS;
@@ -468,7 +467,7 @@ __global__ __launch_bounds__(THREADS) void token_backward_kernel(TokenBackArgs a
       const float y = (v[i] - m) - log_s, p = exp_hw(y);
       o[i] = p * (ENT ? dl - de * (fmaxf(y, -1e4f) + h) : dl);
     }
-    if (nothing) {
+    if (nothing) {  // whatever the row holds
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i] = 0.f;
     }
