@@ -593,9 +593,6 @@ MAO_API mao_status mao_linear_backward_weight(mao_mat dY, const mao_mat* X, cons
  * entropy 0 and no gradient; one with a NaN or +inf has NaN results.
  */
 
-/* Workspace bytes (0 when none is needed or an argument is invalid). */
-MAO_API size_t mao_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int32_t top);
-
 /*
  * mao_token_logprobs -- with M = max_j x_j and S = sum_j e^(x_j - M) of each row:
  *   logprob = (x_target - M) - log S;  entropy = -sum_j p_j log p_j;
@@ -606,8 +603,7 @@ MAO_API size_t mao_token_logprobs_workspace_size(int64_t rows, int64_t vocab, in
  */
 MAO_API mao_status mao_token_logprobs(mao_mat X, const int64_t* targets, float* logprob,
                                       float* entropy, float* stats, int32_t top,
-                                      float* top_logprobs, int64_t* top_ids, void* workspace,
-                                      size_t workspace_bytes, void* stream);
+                                      float* top_logprobs, int64_t* top_ids, void* stream);
 
 /*
  * mao_token_logprobs_backward -- from the gradients of logprob, entropy and lse = M + log S

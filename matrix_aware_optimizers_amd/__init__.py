@@ -152,9 +152,8 @@ EXPORTS = {
                                             POINTER(Mat), Mat, c_void_p, c_size_t, c_void_p]),
     "mao_linear_backward_weight": (c_int32, [Mat, POINTER(Mat), POINTER(Q8C), c_int32, Mat,
                                              c_void_p, c_int32, c_void_p, c_size_t, c_void_p]),
-    "mao_token_logprobs_workspace_size": (c_size_t, [c_int64, c_int64, c_int32]),
     "mao_token_logprobs": (c_int32, [Mat, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p,
-                                     c_void_p, c_void_p, c_size_t, c_void_p]),
+                                     c_void_p, c_void_p]),
     "mao_token_logprobs_backward": (c_int32, [Mat, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                               c_void_p, Mat, c_void_p]),
     "mao_token_loss": (c_int32, [Mat, c_void_p, c_void_p, c_void_p, Mat, c_void_p]),

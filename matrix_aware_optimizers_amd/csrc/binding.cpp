@@ -437,12 +437,11 @@ PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
       top_lp = at::empty({x.rows, k}, f);
       ids = at::empty({x.rows, k}, X.options().dtype(at::kLong));
     }
-    const Workspace ws(mao_token_logprobs_workspace_size(x.rows, x.cols, (int32_t)top), dev, stream);
     check(mao_token_logprobs(x, targets, targets ? (float*)lp.data_ptr() : nullptr,
                              ent.defined() ? (float*)ent.data_ptr() : nullptr,
                              (float*)stats.data_ptr(), (int32_t)top,
                              k ? (float*)top_lp.data_ptr() : nullptr,
-                             k ? (int64_t*)ids.data_ptr() : nullptr, ws.p, ws.bytes, (void*)stream),
+                             k ? (int64_t*)ids.data_ptr() : nullptr, (void*)stream),
           "mao_token_logprobs");
     const auto out = [](const at::Tensor& t) {
       return t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None);

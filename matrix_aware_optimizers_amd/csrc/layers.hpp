@@ -190,8 +190,7 @@ constexpr int kTokenRows = 16;
 mao_status launch_linear_token(int dtype, const LinProblem& p, hipStream_t s);
 
 // ---- log probabilities of tokens (token_probs.hip) ------------------------
-constexpr int kTokenTop = 32;    // alternatives at most
-constexpr int kTokenParts = 16;  // workgroups per row at most
+constexpr int kTokenTop = 32;  // alternatives at most
 
 struct TokenArgs {
   const void* x;
@@ -199,16 +198,9 @@ struct TokenArgs {
   float *logprob, *entropy, *stats;  // or nullptr; stats: (maximum, log of the sum) per row
   float* top_logprobs;
   int64_t* top_ids;
-  float* part_sums;     // 4 per part
-  uint64_t* part_keys;  // `top` per part
   int64_t ldx;
   int rows, vocab, top;
-  int parts, part_runs;  // workgroups per row, runs of 8 logits for each
 };
-struct TokenCut {
-  int parts, part_runs;
-};
-TokenCut token_cut(int64_t rows, int64_t vocab);
 mao_status launch_tokens(const TokenArgs& a, int dtype, hipStream_t s);
 
 struct TokenBackArgs {
@@ -221,7 +213,7 @@ struct TokenBackArgs {
   void* dx;                                 // may be x
   int64_t ldx, lddx;
   int rows, vocab, dx_dtype;
-  int parts, part_runs;  // set by the launch
+  int parts, part_runs;  // workgroups per row, pieces for each: set by the launch
 };
 mao_status launch_tokens_backward(const TokenBackArgs& a, int dtype, hipStream_t s);
 mao_status launch_token_loss(const TokenBackArgs& a, int dtype, hipStream_t s);

@@ -110,23 +110,6 @@ WeightWs carve_weight(void* base, int64_t rows, int64_t k, int64_t n, int dtype,
   return w;
 }
 
-// The parts of a row's work: sums, then alternatives.
-struct TokenWs {
-  float* sums;
-  uint64_t* keys;
-  size_t bytes;
-};
-TokenWs carve_tokens(void* base, int64_t rows, int64_t vocab, int top) {
-  const TokenCut cut = token_cut(rows, vocab);
-  Carver c(base);
-  TokenWs w = {};
-  if (cut.parts == 1) return w;
-  w.sums = c.take<float>((size_t)rows * cut.parts * 4);
-  if (top) w.keys = c.take<uint64_t>((size_t)rows * cut.parts * top);
-  w.bytes = c.used;
-  return w;
-}
-
 constexpr int64_t kMostBlocks = (1 << 24) - 1;  // of 256 threads: a launch has below 2^32
 
 mao_status check_targets(const int64_t* t) {
@@ -494,14 +477,9 @@ mao_status mao_linear_backward_weight(mao_mat dY, const mao_mat* X, const mao_q8
   return MAO_OK;
 }
 
-size_t mao_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int32_t top) {
-  if (!sizes_ok(rows, vocab, 1) || top < 0 || top > kTokenTop || top > vocab) return 0;
-  return carve_tokens(nullptr, rows, vocab, top).bytes;
-}
-
 mao_status mao_token_logprobs(mao_mat X, const int64_t* targets, float* logprob, float* entropy,
                               float* stats, int32_t top, float* top_logprobs, int64_t* top_ids,
-                              void* workspace, size_t workspace_bytes, void* stream) {
+                              void* stream) {
   MAO_TRY(check_view("X", X));
   if ((targets != nullptr) != (logprob != nullptr)) MAO_FAIL(MAO_E_NULL, "targets and logprob go together");
   if (top < 0 || top > kTokenTop || top > X.cols)
@@ -515,19 +493,15 @@ mao_status mao_token_logprobs(mao_mat X, const int64_t* targets, float* logprob,
   MAO_TRY(check_floats("stats", stats));
   MAO_TRY(check_floats("top_logprobs", top_logprobs));
   if ((uintptr_t)top_ids % 8 != 0) MAO_FAIL(MAO_E_LAYOUT, "top_ids misaligned");
-  const TokenWs w = carve_tokens(workspace, X.rows, X.cols, top);
-  MAO_TRY(check_workspace(workspace, workspace_bytes, w.bytes));
   Buffers b;
   if (logprob) b.out(range_of(logprob, X.rows * 4));
   if (entropy) b.out(range_of(entropy, X.rows * 4));
   if (stats) b.out(range_of(stats, X.rows * 8));
   if (top) b.out(range_of(top_logprobs, X.rows * top * 4));
   if (top) b.out(range_of(top_ids, X.rows * top * 8));
-  if (w.bytes) b.out(range_of(workspace, (int64_t)w.bytes));
   b.in(range_of(X));
   if (targets) b.in(range_of(targets, X.rows * 8));
   MAO_TRY(b.check());
-  const TokenCut cut = token_cut(X.rows, X.cols);
   TokenArgs a = {};
   a.x = X.data;
   a.ldx = X.ld;
@@ -540,10 +514,6 @@ mao_status mao_token_logprobs(mao_mat X, const int64_t* targets, float* logprob,
   a.top = top;
   a.top_logprobs = top_logprobs;
   a.top_ids = top_ids;
-  a.parts = cut.parts;
-  a.part_runs = cut.part_runs;
-  a.part_sums = w.sums;
-  a.part_keys = w.keys;
   return launch_tokens(a, X.dtype, (hipStream_t)stream);
 }
 
@@ -563,7 +533,7 @@ mao_status mao_token_logprobs_backward(mao_mat X, const int64_t* targets, const 
   MAO_TRY(check_floats("dlogprob", dlogprob));
   MAO_TRY(check_floats("dentropy", dentropy));
   MAO_TRY(check_floats("dlse", dlse));
-  if (X.rows * ceil_div(X.cols, 8192) > kMostBlocks) MAO_FAIL(MAO_E_UNSUPPORTED, "more than 2^32 threads");
+  if (X.rows * ceil_div(X.cols, 2048) > kMostBlocks) MAO_FAIL(MAO_E_UNSUPPORTED, "more than 2^32 threads");
   Buffers b;
   b.out(range_of(dX));
   if (!same_view(X, dX)) b.in(range_of(X));

@@ -84,7 +84,7 @@ __device__ __forceinline__ void add_runs(Sums& q, const float (&v)[R][8]) {
   if (ENT) q.t += (t[0] + t[1]) + (t[2] + t[3]);
 }
 
-// Sums over the block's threads, in every thread. buf: 3 floats per wavefront, used once.
+// Sums over the block's threads, in every thread. buf: 3 floats per wavefront, for one call.
 template <int THREADS>
 __device__ __forceinline__ Sums block_sums(Sums q, float (*buf)[3]) {
   const float m = wave_max(q.m);
@@ -131,36 +131,82 @@ __device__ __forceinline__ uint64_t key_of(float x, int token) {
 
 constexpr int kList = 1024;  // candidates that fit
 
-struct TopShared {
+template <int THREADS> struct TopShared {
   uint64_t list[kList];
   uint32_t group[64];
   uint32_t hist[256];
-  uint32_t count, limit, need;
+  uint32_t count, lines, limit, need;
+  uint16_t line[THREADS];  // threads whose runs are looked through
 };
 
-// The `top` largest keys of the runs [lo, hi) of a row, each handed to emit with its place
-// in the order; places past the part's elements get key 0. m: the largest logit of this
-// thread's runs, which `kept` holds if KEEP (one block of R a thread).
+// The `top` largest keys of a row, each handed to emit with its place in the order. m: the largest
+// logit of this thread's runs, which `kept` holds if KEEP (R of them).
 //
 // The threads form 64 groups; the top-th largest of the groups' maxima (its upper 16 bits)
-// is a limit that at least `top` logits reach and, of logits in no order, few more do. Threads
-// whose own maximum reaches it look through their runs. Where too many reach it (ties; a
-// mask that leaves a few neighbours), the exact limit is found by four histograms of 8
-// bits each, and of the logits equal to it the lowest tokens are taken.
+// is a limit that at least `top` logits reach and, of logits in no order, few more do. The
+// runs of threads whose own maximum reaches it are looked through once more, by all threads.
+// Where too many reach it (ties), the exact limit is found by four histograms of 8 bits
+// each, and of the logits equal to it the lowest tokens are taken. Masked logits are left
+// out of that: where the others are fewer than `top`, the lowest masked tokens follow.
 template <int THREADS>
-__device__ __forceinline__ void group_maxima(float m, bool any, TopShared& sh) {
+__device__ __forceinline__ void group_maxima(float m, bool any, TopShared<THREADS>& sh) {
   constexpr int GROUP = THREADS / 64;
   uint32_t g = any ? ordered(m) : 0;
 #pragma unroll
   for (int off = 1; off < GROUP; off <<= 1) g = max(g, (uint32_t)__shfl_xor((int)g, off, 64));
   if ((threadIdx.x & (GROUP - 1)) == 0) sh.group[threadIdx.x / GROUP] = g;
-  if (threadIdx.x == 0) sh.count = 0;
+  if (threadIdx.x == 0) sh.count = sh.lines = 0;
 }
+
+// Hands the lowest `need` tokens (at most) whose logit is `equal` to emit, from place `at` on.
+template <typename T, int THREADS, typename Emit>
+__device__ void lowest_tokens(const T* x, int vocab, int runs, uint32_t equal, int at,
+                              int need, TopShared<THREADS>& sh, Emit emit) {
+  const int tid = threadIdx.x;
+  int found = 0;
+  for (int base = 0; found < need && base < runs; base += THREADS) {
+    const int run = base + tid;
+    uint32_t mine = 0;
+    if (run < runs) {
+      float v[8];
+      load_logits(x, run, vocab, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (8 * run + i < vocab && ordered(v[i]) == equal) mine |= 1u << i;
+    }
+    // how many lie in the runs before this one
+    int before = __popc(mine);
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int o = __shfl_up(before, off, 64);
+      if ((tid & 63) >= off) before += o;
+    }
+    __syncthreads();
+    if ((tid & 63) == 63) sh.group[tid >> 6] = (uint32_t)before;
+    __syncthreads();
+    before -= __popc(mine);
+    int all = 0;
+    for (int w = 0; w < THREADS / 64; ++w) {
+      if (w < tid >> 6) before += (int)sh.group[w];
+      all += (int)sh.group[w];
+    }
+    before += found;
+    for (int i = 0; i < 8; ++i)
+      if (mine >> i & 1) {
+        if (before < need) emit(at + before, key_of(unordered(equal), 8 * run + i));
+        ++before;
+      }
+    found += all;
+  }
+}
+
+constexpr uint32_t kMasked = 0x007fffffu;  // ordered(-inf)
 
 // After group_maxima and a barrier.
 template <typename T, int THREADS, bool KEEP, int R, typename Emit>
-__device__ __forceinline__ void select_top(const T* x, int vocab, int lo, int hi, int top, float m,
-                                           const float (&kept)[R][8], TopShared& sh, Emit emit) {
+__device__ __forceinline__ void select_top(const T* x, int vocab, int runs, int top, float m,
+                                           const float (&kept)[R][8], TopShared<THREADS>& sh,
+                                           Emit emit) {
   const int tid = threadIdx.x;
   uint32_t limit = 0;
   {
@@ -171,6 +217,7 @@ __device__ __forceinline__ void select_top(const T* x, int vocab, int lo, int hi
       if (__popcll(__ballot(g >= higher)) >= top) limit = higher;
     }
   }
+  limit = max(limit, kMasked + 1);
   auto offer = [&](const float (&v)[8], int run) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -180,17 +227,30 @@ __device__ __forceinline__ void select_top(const T* x, int vocab, int lo, int hi
       }
     }
   };
-  if (lo + tid < hi && ordered(m) >= limit) {
-    if constexpr (KEEP) {
+  const bool reaches = tid < runs && ordered(m) >= limit;
+  if constexpr (KEEP) {
+    if (reaches) {
 #pragma unroll
       for (int r = 0; r < R; ++r)
-        if (lo + tid + r * THREADS < hi) offer(kept[r], lo + tid + r * THREADS);
-    } else {
-      for (int run = lo + tid; run < hi; run += THREADS) {
-        float v[8];
-        load_logits(x, run, vocab, v);
-        offer(v, run);
+        if (tid + r * THREADS < runs) offer(kept[r], tid + r * THREADS);
+    }
+  } else {
+    if (reaches) sh.line[atomicAdd(&sh.lines, 1u)] = (uint16_t)tid;
+    __syncthreads();
+    // run r of thread line[l] for all r and l, four at a time
+    const int lines = (int)sh.lines, all = lines * ((runs + THREADS - 1) / THREADS);
+    for (int k0 = tid; k0 < all; k0 += 4 * THREADS) {
+      float v[4][8];
+      int run[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int k = k0 + u * THREADS, r = k / lines;
+        run[u] = k < all ? r * THREADS + sh.line[k - r * lines] : runs;
+        load_logits(x, run[u] < runs ? run[u] : 0, vocab, v[u]);
       }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (run[u] < runs) offer(v[u], run[u]);
     }
   }
   __syncthreads();
@@ -202,14 +262,21 @@ __device__ __forceinline__ void select_top(const T* x, int vocab, int lo, int hi
       __syncthreads();
       for (int b = tid; b < 256; b += THREADS) sh.hist[b] = 0;
       __syncthreads();
-      for (int run = lo + tid; run < hi; run += THREADS) {
+      for (int run = tid; run < runs; run += THREADS) {
         float v[8];
         load_logits(x, run, vocab, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint32_t k = ordered(v[i]);
-          if (8 * run + i < vocab && (shift == 24 || (k ^ prefix) >> (shift + 8) == 0))
-            atomicAdd(&sh.hist[k >> shift & 255], 1u);
+          const uint32_t k = ordered(v[i]), bin = k >> shift & 255;
+          const bool in = 8 * run + i < vocab && (shift == 24 || (k ^ prefix) >> (shift + 8) == 0);
+          // lanes of one bin (equal logits, most often) add together
+          const uint64_t in_lanes = __ballot(in);
+          if (in_lanes == 0) continue;
+          const int first = __ffsll((unsigned long long)in_lanes) - 1;
+          const uint32_t one = (uint32_t)__builtin_amdgcn_readlane((int)bin, first);
+          const uint64_t same = __ballot(in && bin == one);
+          if ((tid & 63) == first) atomicAdd(&sh.hist[one], (uint32_t)__popcll(same));
+          if (in && bin != one) atomicAdd(&sh.hist[bin], 1u);
         }
       }
       __syncthreads();
@@ -224,60 +291,27 @@ __device__ __forceinline__ void select_top(const T* x, int vocab, int lo, int hi
       prefix |= sh.limit << shift;
     }
     // larger ones, fewer than top, in any order; then the lowest tokens of the equal ones
-    const uint32_t need = sh.need;
+    const int need = (int)sh.need, above = top - need;
     __syncthreads();
     if (tid == 0) sh.count = 0;
     __syncthreads();
-    for (int run = lo + tid; run < hi; run += THREADS) {
-      float v[8];
-      load_logits(x, run, vocab, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (8 * run + i < vocab && ordered(v[i]) > prefix)
-          sh.list[atomicAdd(&sh.count, 1u)] = key_of(v[i], 8 * run + i);
-    }
-    __syncthreads();
-    const uint32_t above = (uint32_t)top - need;
-    uint32_t found = 0;
-    for (int base = lo; found < need && base < hi; base += THREADS) {
-      const int run = base + tid;
-      uint32_t mine = 0;
-      if (run < hi) {
+    if (above > 0) {
+      for (int run = tid; run < runs; run += THREADS) {
         float v[8];
         load_logits(x, run, vocab, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (8 * run + i < vocab && ordered(v[i]) == prefix) mine |= 1u << i;
+          if (8 * run + i < vocab && ordered(v[i]) > prefix)
+            sh.list[atomicAdd(&sh.count, 1u)] = key_of(v[i], 8 * run + i);
       }
-      // how many lie in the runs before this one
-      uint32_t before = (uint32_t)__popc(mine);
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const uint32_t o = (uint32_t)__shfl_up((int)before, off, 64);
-        if ((tid & 63) >= off) before += o;
-      }
-      __syncthreads();
-      if ((tid & 63) == 63) sh.group[tid >> 6] = before;
-      __syncthreads();
-      before -= (uint32_t)__popc(mine);
-      uint32_t all = 0;
-      for (int w = 0; w < THREADS / 64; ++w) {
-        if (w < tid >> 6) before += sh.group[w];
-        all += sh.group[w];
-      }
-      before += found;
-      for (int i = 0; i < 8; ++i)
-        if (mine >> i & 1) {
-          if (before < need) sh.list[above + before] = key_of(unordered(prefix), 8 * run + i);
-          ++before;
-        }
-      found += all;
     }
+    lowest_tokens<T, THREADS>(x, vocab, runs, prefix, above, need, sh, emit);
     __syncthreads();
-    if (tid == 0) sh.count = (uint32_t)top;
-    __syncthreads();
+  } else if ((int)sh.count < top) {
+    // fewer than top that are not masked
+    lowest_tokens<T, THREADS>(x, vocab, runs, kMasked, (int)sh.count, top - (int)sh.count, sh, emit);
   }
-  // in order by counting the larger ones: keys are distinct, and at least min(top, elements)
+  // in order by counting the larger ones: keys are distinct
   const int n = (int)sh.count;
   for (int c = tid; c < n; c += THREADS) {
     const uint64_t mine = sh.list[c];
@@ -286,7 +320,6 @@ __device__ __forceinline__ void select_top(const T* x, int vocab, int lo, int hi
     for (int j = 0; j < n; ++j) rank += sh.list[j] > mine;
     if (rank < top) emit(rank, mine);
   }
-  for (int k = n + tid; k < top; k += THREADS) emit(k, 0);
 }
 
 // What a row's sums give.
@@ -323,130 +356,152 @@ __device__ __forceinline__ void write_top(const TokenArgs& a, int64_t row, const
   if (a.top_ids) a.top_ids[at] = bad ? -1 : (int64_t)(uint32_t)~(uint32_t)key;
 }
 
-// One workgroup per part of a row; parts == 1: the row's results, else the part's sums
-// (a.part_sums) and alternatives (a.part_keys). KEEP: the part is one block of R runs a thread.
+// A row per workgroup, in blocks of R runs a thread. KEEP: the row is one block.
 template <typename T, int THREADS, bool ENT, bool TOP, bool KEEP>
 __global__ __launch_bounds__(THREADS) void token_kernel(TokenArgs a) {
   constexpr int R = 4;
   __shared__ float buf[THREADS / 64][3];
-  const uint32_t line = blockIdx.x / (uint32_t)a.parts;
-  const int64_t row = line;
-  const int part = (int)(blockIdx.x - line * (uint32_t)a.parts);
+  const int64_t row = blockIdx.x;
   const T* x = (const T*)a.x + row * a.ldx;
   const int runs = (a.vocab + 7) >> 3;
-  const int lo = part * a.part_runs, hi = min(runs, lo + a.part_runs);
   Sums q;
   q.init();
   float v[R][8];
-  int base = lo + (int)threadIdx.x;
+  int base = (int)threadIdx.x;
   do {
     Raw8<T> raw[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int run = base + r * THREADS;
-      // past the end: the part's first run once more, replaced below
-      raw[r].load_cut(x + 8 * (int64_t)(run < hi ? run : lo), run < hi ? a.vocab - 8 * run : 8);
+      // past the end: the row's first run once more, replaced below
+      raw[r].load_cut(x + 8 * (int64_t)(run < runs ? run : 0), run < runs ? a.vocab - 8 * run : 8);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int run = base + r * THREADS;
       raw[r].get(v[r]);
-      const int valid = run < hi ? a.vocab - 8 * run : 0;
+      const int valid = run < runs ? a.vocab - 8 * run : 0;
       if (valid < 8) cut_run(v[r], valid);
     }
-    add_runs<ENT, R>(q, v);
+    if (KEEP && runs <= R / 2 * THREADS)
+      add_runs<ENT, R / 2>(q, (const float(&)[R / 2][8])v);
+    else
+      add_runs<ENT, R>(q, v);
     base += R * THREADS;
-  } while (!KEEP && base < hi);
+  } while (!KEEP && base < runs);
   if constexpr (TOP) {
-    __shared__ TopShared sh;
-    // kNone: masked logits alone, or none that is larger than the lowest number
-    const float mine = q.m == kNone ? -INFINITY : q.m;
-    group_maxima<THREADS>(mine, lo + (int)threadIdx.x < hi, sh);
+    __shared__ TopShared<THREADS> sh;
+    const float mine = q.m;
+    group_maxima<THREADS>(mine, (int)threadIdx.x < runs, sh);
     if constexpr (THREADS == 64) __syncthreads();
     q = block_sums<THREADS>(q, buf);
-    if (a.parts == 1) {
-      auto out = [&](int k, uint64_t key) { write_top(a, row, q, k, key); };
-      if (q.s == q.s)
-        select_top<T, THREADS, KEEP, R>(x, a.vocab, lo, hi, a.top, mine, v, sh, out);
-      else
-        for (int k = threadIdx.x; k < a.top; k += THREADS) out(k, 0);
-    } else {
-      uint64_t* keys = a.part_keys + (int64_t)blockIdx.x * a.top;
-      auto out = [&](int k, uint64_t key) { keys[k] = key; };
-      if (q.s == q.s)
-        select_top<T, THREADS, KEEP, R>(x, a.vocab, lo, hi, a.top, mine, v, sh, out);
-      else
-        for (int k = threadIdx.x; k < a.top; k += THREADS) out(k, 0);
-    }
+    auto out = [&](int k, uint64_t key) { write_top(a, row, q, k, key); };
+    if (q.s == q.s)
+      select_top<T, THREADS, KEEP, R>(x, a.vocab, runs, a.top, mine, v, sh, out);
+    else
+      for (int k = threadIdx.x; k < a.top; k += THREADS) out(k, 0);
   } else {
     q = block_sums<THREADS>(q, buf);
   }
-  if (threadIdx.x != 0) return;
-  if (a.parts == 1) {
-    write_row<T>(a, row, q);
-  } else {
-    float* p = a.part_sums + 4 * (int64_t)blockIdx.x;
-    p[0] = q.m;
-    p[1] = q.s;
-    p[2] = q.t;
-  }
+  if (threadIdx.x == 0) write_row<T>(a, row, q);
 }
 
-// The join of a row's parts: one workgroup per row, of one wavefront without alternatives.
-template <typename T, bool TOP>
-__global__ __launch_bounds__(TOP ? 256 : 64) void token_join_kernel(TokenArgs a) {
-  const int64_t row = blockIdx.x;
-  const int tid = threadIdx.x, lane = tid & 63;
-  Sums q;
-  q.init();
-  if (lane < a.parts) {
-    const float* p = a.part_sums + 4 * (row * a.parts + lane);
-    q.m = p[0];
-    q.s = p[1];
-    q.t = p[2];
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// A row for buffer instructions: past its `bytes` they read 0 and write nothing. One offset
+// register serves every access of a thread (64-bit addresses of the pieces of two rows took 93
+// registers where 64 let two workgroups share a CU).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const void* p, int64_t row_bytes,
+                                                             int row, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((char*)p + row_bytes * row, 0, bytes, 0x00027000);
+}
+
+// Gradients work on pieces of 16 bytes: consecutive lanes read consecutive ones. (fp32 in
+// runs of 8, of which each load takes every other 16 bytes: 2045 x 50301 167 us for 145.)
+template <typename T> struct Piece {
+  static constexpr int W = 16 / sizeof(T);
+  u32x4 a;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t row, int piece) {
+    a = __builtin_amdgcn_raw_buffer_load_b128(row, piece * 16, 0, 0);
   }
-  if constexpr (TOP) {
-    constexpr int kMost = kTokenParts * kTokenTop;
-    __shared__ uint64_t keys[kMost];
-    const int n = a.parts * a.top;
-    for (int k = tid; k < n; k += 256) keys[k] = a.part_keys[row * n + k];
-    q.raise(wave_max(q.m));
-    q.s = wave_total(q.s);
-    q.t = wave_total(q.t);
-    __syncthreads();
-    for (int k = tid; k < n; k += 256) {
-      const uint64_t mine = keys[k];
-      if (mine == 0 && q.s == q.s) continue;  // no element
-      int rank = 0;
-      // equal ones only in a row with a NaN, whose parts have none
-#pragma unroll 8
-      for (int j = 0; j < n; ++j) rank += keys[j] > mine || (keys[j] == mine && j < k);
-      if (rank < a.top) write_top(a, row, q, rank, mine);
+  // the compiler may not carry values derived from here on across this point
+  __device__ __forceinline__ void opaque() {
+    asm volatile("" : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3]));
+  }
+  __device__ __forceinline__ void get(float (&v)[W]) const {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if (W == 4)
+        v[i] = __uint_as_float(a[i]);
+      else
+        v[i] = __uint_as_float(i & 1 ? a[i >> 1] & 0xffff0000u : a[i >> 1] << 16);
     }
-  } else {
-    q.raise(wave_max(q.m));
-    q.s = wave_total(q.s);
-    q.t = wave_total(q.t);
   }
-  if (tid == 0) write_row<T>(a, row, q);
-}
+};
 
-// The gradient, a segment of a row per workgroup. ENT: the entropy's too.
-template <typename T, typename TO, int THREADS, bool ENT>
+// A row of results, written past the L2 (the next reader is another kernel, and the rows are
+// larger): 16384 x 50304 bf16 555 us for 577, 16384 x 8000 90 for 102.
+template <int W> struct RowOut {
+  char* p;
+  int dtype, cols;
+  __amdgpu_buffer_rsrc_t buf;  // its whole pieces
+  __device__ __forceinline__ RowOut(void* base, int dt, int64_t ld, int row, int n)
+      : dtype(dt), cols(n) {
+    const int es = dt == MAO_BF16 ? 2 : 4;
+    p = (char*)base + ld * es * row;
+    buf = row_buffer(base, ld * es, row, n / W * W * es);
+  }
+  __device__ __forceinline__ void store(int piece, const float (&v)[W]) const {
+    constexpr int NT = 2;
+    if (dtype == MAO_BF16) {
+      if constexpr (W == 8) {
+        const u32x4 k = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                         pack_bf16x2(v[6], v[7])};
+        __builtin_amdgcn_raw_buffer_store_b128(k, buf, piece * 16, 0, NT);
+      } else {
+        const u32x2 k = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        __builtin_amdgcn_raw_buffer_store_b64(k, buf, piece * 8, 0, NT);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; i += 4) {
+        const u32x4 k = {__float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]),
+                         __float_as_uint(v[i + 3])};
+        __builtin_amdgcn_raw_buffer_store_b128(k, buf, piece * (W * 4) + i * 4, 0, NT);
+      }
+    }
+    const int n = cols - W * piece;
+    if (n > 0 && n < W) {
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        if (i < n) {
+          if (dtype == MAO_BF16)
+            ((bf16_t*)p)[W * piece + i] = f32_to_bf16(v[i]);
+          else
+            ((float*)p)[W * piece + i] = v[i];
+        }
+    }
+  }
+};
+
+// Pieces a thread of the backward pass: 8192 x 50304 bf16 269 us with two, 291 with four, 299
+// with one; 2045 x 50301 fp32 140, 145 and 141.
+constexpr int kBackPieces = 2;
+
+// The gradient, a segment of a row (kBackPieces a thread) per workgroup. ENT: the entropy's too.
+template <typename T, int THREADS, bool ENT>
 __global__ __launch_bounds__(THREADS) void token_backward_kernel(TokenBackArgs a) {
+  constexpr int R = kBackPieces, W = Piece<T>::W;
   const uint32_t line = blockIdx.x / (uint32_t)a.parts;
   const int64_t row = line;
   const int part = (int)(blockIdx.x - line * (uint32_t)a.parts);
-  const int runs = (a.vocab + 7) >> 3;
-  const int lo = part * a.part_runs, hi = min(runs, lo + a.part_runs);
-  const T* x = (const T*)a.x + row * a.ldx;
-  constexpr int R = 4;  // a segment is one block of runs
-  Raw8<T> raw[R];
+  const int lo = part * a.part_runs + (int)threadIdx.x, hi = (part + 1) * a.part_runs;
+  const auto x = row_buffer(a.x, a.ldx * (int64_t)sizeof(T), (int)line, (a.vocab + W - 1) / W * 16);
+  const RowOut<W> out(a.dx, a.dx_dtype, a.lddx, (int)line, a.vocab);
+  Piece<T> raw[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int run = lo + (int)threadIdx.x + r * THREADS;
-    if (run < hi) raw[r].load_cut(x + 8 * (int64_t)run, a.vocab - 8 * run);
-  }
+  for (int r = 0; r < R; ++r) raw[r].load(x, lo + r * THREADS);
   const int64_t target = a.targets ? a.targets[row] : -1;
   const float m = a.stats[2 * row], log_s = a.stats[2 * row + 1];
   float dlp = a.dlogprob && target >= 0 ? a.dlogprob[row] : 0.f;
@@ -458,174 +513,168 @@ __global__ __launch_bounds__(THREADS) void token_backward_kernel(TokenBackArgs a
   const bool nothing = empty || (dl == 0.f && de == 0.f);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int run = lo + (int)threadIdx.x + r * THREADS;
-    if (run >= hi) break;
-    float v[8], o[8];
+    const int piece = lo + r * THREADS;
+    if (piece >= hi) break;
+    float v[W], o[W];
     raw[r].get(v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < W; ++i) {
       const float y = (v[i] - m) - log_s, p = exp_hw(y);
       o[i] = p * (ENT ? dl - de * (fmaxf(y, -1e4f) + h) : dl);
     }
     if (nothing) {  // whatever the row holds
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = 0.f;
+      for (int i = 0; i < W; ++i) o[i] = 0.f;
     }
-    const int64_t at = target - 8 * (int64_t)run;
-    if (at >= 0 && at < 8) {
+    const int64_t at = target - W * (int64_t)piece;
+    if (at >= 0 && at < W) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] += i == (int)at ? dlp : 0.f;
+      for (int i = 0; i < W; ++i) o[i] += i == (int)at ? dlp : 0.f;
     }
-    store8n_any(a.dx, sizeof(TO) == 2 ? MAO_BF16 : MAO_F32, row * a.lddx + 8 * (int64_t)run, o,
-                a.vocab - 8 * run);
+    out.store(piece, o);
   }
 }
 
+template <int W>
+__device__ __forceinline__ void add_piece(Sums& q, float (&v)[W], int valid) {
+  if (valid < W) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = i < valid ? v[i] : -INFINITY;
+  }
+  float c = max3(v[0], v[1], v[2]);
+  c = max3(c, v[3], v[W - 1]);
+  if constexpr (W == 8) {
+    c = max3(c, v[4], v[5]);
+    c = max3(c, v[6], c);
+  }
+  if (c > q.m) q.raise(c);
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < W; ++i) s[i & 3] += exp_hw(v[i] - q.m);
+  q.s += (s[0] + s[1]) + (s[2] + s[3]);
+}
+
 // Log probability and the gradient of -w logprob, a row per workgroup. KEEP: the row stays in
-// registers (R runs of 8 a thread), else it is read twice.
+// registers (R pieces a thread), else it is read twice. (Workgroups that go on to a next row and
+// read it as they write, 1 to 4 of them at a time per place on the CUs: 610 to 617 us on
+// 16384 x 50304 bf16, 540 with a workgroup for each row.)
 template <typename T, int THREADS, int R, bool KEEP>
 __global__ __launch_bounds__(THREADS) void token_loss_kernel(TokenBackArgs a) {
+  constexpr int W = Piece<T>::W;
   __shared__ float buf[THREADS / 64][3];
-  const int64_t row = blockIdx.x;
-  const int runs = (a.vocab + 7) >> 3, tid = threadIdx.x;
-  const T* x = (const T*)a.x + row * a.ldx;
+  const int pieces = (a.vocab + W - 1) / W, tid = threadIdx.x, row = blockIdx.x;
   const int64_t target = a.targets[row];
-  const int out_type = a.dx_dtype;
-  if (target < 0) {  // nothing of the row matters
-    const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int run = tid; run < runs; run += THREADS)
-      store8n_any(a.dx, out_type, row * a.lddx + 8 * (int64_t)run, zero, a.vocab - 8 * run);
-    if (tid == 0 && a.logprob) a.logprob[row] = 0.f;
-    return;
-  }
-  float w = a.weight ? a.weight[row] : 1.f;
-  if (target >= a.vocab) {
-    w = NAN;
-    if (tid == 0 && a.logprob) a.logprob[row] = NAN;
-  }
-  Raw8<T> raw[R];
+  const bool live = target >= 0;  // else nothing of the row matters
+  const int hit = target < a.vocab ? (int)target : -1;
+  // a row that does not matter is not read
+  const auto x = row_buffer(a.x, a.ldx * (int64_t)sizeof(T), row, live ? pieces * 16 : 0);
+  const RowOut<W> out(a.dx, a.dx_dtype, a.lddx, row, a.vocab);
+  Piece<T> raw[R];
   Sums q;
   q.init();
-  if constexpr (KEEP) {
+  for (int base = tid; base < pieces; base += THREADS * R) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) raw[r].load(x, base + r * THREADS);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int run = tid + r * THREADS;
-      if (run < runs) raw[r].load_cut(x + 8 * (int64_t)run, a.vocab - 8 * run);
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int run = tid + r * THREADS;
-      if (run < runs) {
-        float v[1][8];
-        raw[r].get(v[0]);
-        if (a.vocab - 8 * run < 8) cut_run(v[0], a.vocab - 8 * run);
-        add_runs<false, 1>(q, v);
+      const int piece = base + r * THREADS;
+      if (piece < pieces) {
+        float v[W];
+        raw[r].get(v);
+        add_piece<W>(q, v, a.vocab - W * piece);
       }
     }
-  } else {
-    for (int base = tid; base < runs; base += THREADS * R) {
-      float v[R][8];
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int run = base + r * THREADS;
-        raw[r].load_cut(x + 8 * (int64_t)(run < runs ? run : 0), run < runs ? a.vocab - 8 * run : 8);
-      }
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int run = base + r * THREADS;
-        raw[r].get(v[r]);
-        const int valid = run < runs ? a.vocab - 8 * run : 0;
-        if (valid < 8) cut_run(v[r], valid);
-      }
-      add_runs<false, R>(q, v);
-    }
+    if (KEEP) break;
   }
   // dx may be x: a thread writes what it alone has read
   q = block_sums<THREADS>(q, buf);
+  float w = a.weight && live ? a.weight[row] : 1.f;
+  if (target >= a.vocab) w = NAN;
   if (q.s == 0.f) w = 0.f;  // no finite logit
   const float scale = q.s == 0.f ? 0.f : w / q.s;
-  auto finish = [&](int run, float (&v)[8]) __attribute__((always_inline)) {
-    const int64_t at = target - 8 * (int64_t)run;
+  if (a.logprob && hit < 0 && tid == 0) a.logprob[row] = live ? NAN : 0.f;
+  auto finish = [&](Piece<T>& k, int piece) __attribute__((always_inline)) {
+    float v[W];
+    k.opaque();
+    k.get(v);
+    const int at = hit - W * piece;
+    const bool here = hit >= 0 && at >= 0 && at < W;
     float xt = 0.f;
-    if (at >= 0 && at < 8) {
+    if (here) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) xt = i == (int)at ? v[i] : xt;
+      for (int i = 0; i < W; ++i) xt = i == at ? v[i] : xt;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = exp_hw(v[i] - q.m) * scale;
-    if (at >= 0 && at < 8 && target < a.vocab) {
+    for (int i = 0; i < W; ++i) v[i] = live ? exp_hw(v[i] - q.m) * scale : 0.f;
+    if (here) {
       if (a.logprob) a.logprob[row] = log_prob(xt, q, q.s == 0.f ? 0.f : logf(q.s));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] -= i == (int)at ? w : 0.f;
+      for (int i = 0; i < W; ++i) v[i] -= i == at ? w : 0.f;
     }
-    store8n_any(a.dx, out_type, row * a.lddx + 8 * (int64_t)run, v, a.vocab - 8 * run);
+    out.store(piece, v);
   };
-  if constexpr (KEEP) {
+  for (int base = tid; base < pieces; base += THREADS * R) {
+    if (!KEEP) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int run = tid + r * THREADS;
-      if (run < runs) {
-        float v[8];
-        raw[r].opaque();
-        raw[r].get(v);
-        finish(run, v);
-      }
+      for (int r = 0; r < R; ++r) raw[r].load(x, base + r * THREADS);
     }
-  } else {
-    for (int run = tid; run < runs; run += THREADS) {
-      float v[8];
-      raw[0].load_cut(x + 8 * (int64_t)run, a.vocab - 8 * run);
-      raw[0].get(v);
-      finish(run, v);
-    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (base + r * THREADS < pieces) finish(raw[r], base + r * THREADS);
+    if (KEEP) break;
   }
 }
 
 template <typename T, int THREADS, bool KEEP>
 mao_status forward_go(const TokenArgs& a, hipStream_t s) {
-  const dim3 grid((uint32_t)((int64_t)a.rows * a.parts));
   const bool ent = a.entropy != nullptr, top = a.top != 0;
 #define MAO_TOKEN(E, P) \
-  hipLaunchKernelGGL((token_kernel<T, THREADS, E, P, KEEP>), grid, dim3(THREADS), 0, s, a)
+  hipLaunchKernelGGL((token_kernel<T, THREADS, E, P, KEEP>), dim3(a.rows), dim3(THREADS), 0, s, a)
   if (ent && top) MAO_TOKEN(true, true);
   else if (ent) MAO_TOKEN(true, false);
   else if (top) MAO_TOKEN(false, true);
   else MAO_TOKEN(false, false);
 #undef MAO_TOKEN
   MAO_LAUNCH_CHECK();
-  if (a.parts == 1) return MAO_OK;
-  if (top)
-    hipLaunchKernelGGL((token_join_kernel<T, true>), dim3(a.rows), dim3(256), 0, s, a);
+  return MAO_OK;
+}
+
+// Threads of a row. Long rows, bf16, no alternatives / 20 of them, in us:
+//   50304: 256 threads 7.4 / 11.8 (1 row), 20.6 / 28.0 (1024 rows); 512 threads 6.4 / 9.4, 20.1 /
+//   26.0; 1024 threads 6.6 / 10.2, 24.1 / 39.2
+//   20000: 256 threads 11.2 / 15.6 (1024 rows), 512 threads 13.2 / 18.8
+// A row over four workgroups and a second kernel to join them took 10 / 11.7 on one row of
+// 50304, gained nothing below 128256 columns or above 256 rows, and was left out (one row of
+// 256000, where a CU's arithmetic bounds it: 10 / 16 for 19 / 23).
+template <typename T>
+mao_status forward_pick(const TokenArgs& a, hipStream_t s) {
+  const int64_t runs = ceil_div(a.vocab, 8);
+  if (runs <= 64 * 4) return forward_go<T, 64, true>(a, s);
+  if (runs <= 256 * 4) return forward_go<T, 256, true>(a, s);
+  if (runs <= 4096) return forward_go<T, 256, false>(a, s);
+  // few very long rows: latency, a row has a CU to itself
+  if (runs > 8192 && a.rows <= 256) return forward_go<T, 1024, false>(a, s);
+  return forward_go<T, 512, false>(a, s);
+}
+
+template <typename T, int THREADS>
+mao_status backward_go(TokenBackArgs a, hipStream_t s) {
+  const int64_t pieces = ceil_div(a.vocab, Piece<T>::W);
+  a.parts = (int)ceil_div(pieces, kBackPieces * THREADS);
+  a.part_runs = (int)ceil_div(pieces, a.parts);
+  const dim3 grid((uint32_t)((int64_t)a.rows * a.parts));
+  if (a.dentropy)
+    hipLaunchKernelGGL((token_backward_kernel<T, THREADS, true>), grid, dim3(THREADS), 0, s, a);
   else
-    hipLaunchKernelGGL((token_join_kernel<T, false>), dim3(a.rows), dim3(64), 0, s, a);
+    hipLaunchKernelGGL((token_backward_kernel<T, THREADS, false>), grid, dim3(THREADS), 0, s, a);
   MAO_LAUNCH_CHECK();
   return MAO_OK;
 }
 
 template <typename T>
-mao_status forward_pick(const TokenArgs& a, hipStream_t s) {
-  if (a.part_runs <= 64 * 4) return forward_go<T, 64, true>(a, s);
-  if (a.part_runs <= 256 * 4) return forward_go<T, 256, true>(a, s);
-  return forward_go<T, 256, false>(a, s);
-}
-
-template <typename T, typename TO, int THREADS>
-mao_status backward_go(TokenBackArgs a, hipStream_t s) {
-  const int64_t runs = ceil_div(a.vocab, 8);
-  a.parts = (int)ceil_div(runs, 4 * THREADS);
-  a.part_runs = (int)ceil_div(runs, a.parts);
-  const dim3 grid((uint32_t)((int64_t)a.rows * a.parts));
-  if (a.dentropy)
-    hipLaunchKernelGGL((token_backward_kernel<T, TO, THREADS, true>), grid, dim3(THREADS), 0, s, a);
-  else
-    hipLaunchKernelGGL((token_backward_kernel<T, TO, THREADS, false>), grid, dim3(THREADS), 0, s, a);
-  MAO_LAUNCH_CHECK();
-  return MAO_OK;
-}
-
-template <typename T, typename TO>
 mao_status backward_pick(const TokenBackArgs& a, hipStream_t s) {
-  return a.vocab <= 64 * 4 * 8 ? backward_go<T, TO, 64>(a, s) : backward_go<T, TO, 256>(a, s);
+  return a.vocab <= 64 * Piece<T>::W * kBackPieces ? backward_go<T, 64>(a, s)
+                                                      : backward_go<T, 256>(a, s);
 }
 
 template <typename T, int THREADS, int R, bool KEEP>
@@ -637,36 +686,25 @@ mao_status loss_go(const TokenBackArgs& a, hipStream_t s) {
 
 template <typename T>
 mao_status loss_pick(const TokenBackArgs& a, hipStream_t s) {
-  const int64_t runs = ceil_div(a.vocab, 8);
-  if (runs <= 64 * 2) return loss_go<T, 64, 2, true>(a, s);
-  if (runs <= 256 * 4) return loss_go<T, 256, 4, true>(a, s);
-  if (runs <= 1024 * 4) return loss_go<T, 1024, 4, true>(a, s);
-  if (runs <= 1024 * 8) return loss_go<T, 1024, 8, true>(a, s);
-  if (sizeof(T) == 2 && runs <= 1024 * 16) return loss_go<T, 1024, sizeof(T) == 2 ? 16 : 8, true>(a, s);
+  const int64_t pieces = ceil_div(a.vocab, Piece<T>::W);
+  if (pieces <= 64 * 4) return loss_go<T, 64, 4, true>(a, s);
+  if (pieces <= 256 * 4) return loss_go<T, 256, 4, true>(a, s);
+  if (pieces <= 512 * 4) return loss_go<T, 512, 4, true>(a, s);
+  if (pieces <= 1024 * 4) return loss_go<T, 1024, 4, true>(a, s);
+  if (pieces <= 1024 * 8) return loss_go<T, 1024, 8, true>(a, s);
+  if (pieces <= 1024 * 16) return loss_go<T, 1024, 16, true>(a, s);
+  if (pieces <= 1024 * 24) return loss_go<T, 1024, 24, true>(a, s);
   return loss_go<T, 1024, 4, false>(a, s);
 }
 
 }  // namespace
-
-TokenCut token_cut(int64_t rows, int64_t vocab) {
-  // six workgroups per CU, of at least one block of 1024 runs of 8 each
-  const int64_t runs = ceil_div(vocab, 8);
-  int64_t parts = std::min<int64_t>(kTokenParts, ceil_div(6 * 256, rows));
-  parts = std::max<int64_t>(1, std::min(parts, ceil_div(runs, 1024)));
-  const int64_t per = ceil_div(runs, parts);
-  return {(int)ceil_div(runs, per), (int)per};
-}
 
 mao_status launch_tokens(const TokenArgs& a, int dtype, hipStream_t s) {
   return dtype == MAO_BF16 ? forward_pick<bf16_t>(a, s) : forward_pick<float>(a, s);
 }
 
 mao_status launch_tokens_backward(const TokenBackArgs& a, int dtype, hipStream_t s) {
-  if (dtype == MAO_BF16)
-    return a.dx_dtype == MAO_BF16 ? backward_pick<bf16_t, bf16_t>(a, s)
-                                  : backward_pick<bf16_t, float>(a, s);
-  return a.dx_dtype == MAO_BF16 ? backward_pick<float, bf16_t>(a, s)
-                                : backward_pick<float, float>(a, s);
+  return dtype == MAO_BF16 ? backward_pick<bf16_t>(a, s) : backward_pick<float>(a, s);
 }
 
 mao_status launch_token_loss(const TokenBackArgs& a, int dtype, hipStream_t s) {

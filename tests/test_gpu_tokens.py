@@ -91,7 +91,7 @@ VOCABS = [1, 2, 7, 8, 9, 63, 200, 1000, 1024, 1025, 4099, 8192, 8193, 20001, 503
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("vocab", VOCABS)
 def test_forward(gpu_lib, vocab, dtype):
-    """One row (in parts, where it is long), a few, and more than a thousand short ones."""
+    """One row, a few, and more than a thousand short ones."""
     for rows in (1, 7) + ((1300,) if vocab <= 1025 else ()):
         log(f"forward {rows} x {vocab} {dtype}")
         x, t = _logits(vocab + rows, rows, vocab, masked=vocab // 5)
@@ -102,11 +102,12 @@ def test_forward(gpu_lib, vocab, dtype):
 
 
 def test_forward_whole_rows_of_a_batch(gpu_lib):
-    """Enough rows that none is split, long enough for the largest workgroup."""
-    log("forward, whole rows")
-    x, t = _logits(3, 520, 9001)
-    _check_forward(gpu_lib, x, t, "bf16", 20)
-    _check_forward(gpu_lib, x, t, "f32", 32)
+    """Many rows of 256 threads and of 512, of several blocks."""
+    log("forward, rows of a batch")
+    for rows, vocab in ((520, 9001), (300, 70003)):
+        x, t = _logits(3, rows, vocab)
+        _check_forward(gpu_lib, x, t, "bf16", 20)
+        _check_forward(gpu_lib, x, t, "f32", 32)
 
 
 @pytest.mark.parametrize("vocab", [40, 1000, 9000, 50304])
@@ -312,8 +313,8 @@ def test_rows_without_a_target_may_hold_anything(gpu_lib):
     assert (lp[[1, 3, 4]] == 0).all() and (f.logprob[[1, 3, 4]] == 0).all()
 
 
-def test_captured_with_shared_workspaces(gpu_lib):
-    """Two graphs of calls in parts (with workspaces) and a larger eager call between their
+def test_captured(gpu_lib):
+    """Two graphs of calls and a larger eager call between their
     replays: every replay equals the eager results, new logits included."""
     import torch
     log("captured")
@@ -350,7 +351,7 @@ def test_captured_with_shared_workspaces(gpu_lib):
 
 
 def test_two_streams(gpu_lib):
-    """Calls in parts on two streams at once have workspaces of their own."""
+    """Calls on two streams at once."""
     import torch
     log("two streams")
     x1, t1 = _logits(1, 2, 100000)
