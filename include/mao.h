@@ -586,6 +586,57 @@ MAO_API mao_status mao_linear_backward_weight(mao_mat dY, const mao_mat* X, cons
                                               size_t workspace_bytes, void* stream);
 
 /*
+ * Between two blocks: the norm after a block, its gate and scale, the sum with the residual
+ * stream, and the norm before the next block. N(z) = (z - mean) rstd gamma + beta over each
+ * row, as mao_layer_norm (MAO_ROW_NORM_LAYER); with mean = 0 and no beta
+ * (MAO_ROW_NORM_RMS); or z itself (MAO_ROW_NORM_NONE, without parameters). cols <= 16384
+ * (MAO_E_UNSUPPORTED above).
+ */
+typedef enum { MAO_ROW_NORM_NONE = 0, MAO_ROW_NORM_LAYER = 1, MAO_ROW_NORM_RMS = 2 } mao_row_norm_kind;
+
+typedef struct {
+  int32_t kind;                /* mao_row_norm_kind */
+  const void *gamma, *beta;    /* NULL (1, 0) or cols values of param_dtype */
+  int32_t param_dtype;
+  float eps;                   /* > 0 (ignored without a norm) */
+} mao_row_norm;
+
+/*
+ * mao_residual_norm -- R = x_scale X + b_scale gate . N_post(B);  H = N_pre(R).
+ * X and R: one type, R may be X itself. B, H and gates: one type. gate: at most one of a
+ * vector (cols values of gate_dtype) and gates (rows x cols). H: NULL exactly if pre is
+ * MAO_ROW_NORM_NONE; it is made from R before R is rounded to its type. stats: NULL or rows x
+ * 4 floats (16-byte aligned) for the backward pass: mean and rstd of both norms (0 and 1
+ * where there is none).
+ */
+MAO_API mao_status mao_residual_norm(mao_mat X, mao_mat B, const mao_row_norm* post,
+                                     const void* gate, int32_t gate_dtype, const mao_mat* gates,
+                                     float x_scale, float b_scale, const mao_row_norm* pre,
+                                     mao_mat R, const mao_mat* H, float* stats, void* stream);
+
+/* Vector gradients, each NULL or cols floats. */
+typedef struct {
+  float *dpost_gamma, *dpost_beta, *dpre_gamma, *dpre_beta, *dgate;
+} mao_residual_norm_sums;
+
+MAO_API size_t mao_residual_norm_backward_workspace_size(int64_t rows, int64_t cols);
+
+/*
+ * mao_residual_norm_backward -- from dH (NULL exactly if pre is MAO_ROW_NORM_NONE) and dR (NULL,
+ * or the gradient of R from what follows): dX, dB, dGates (NULL, or with gates the gradient of
+ * each) and vector gradients (sums: NULL or those asked for; dgate with a vector gate). B, R and
+ * stats as in the forward call (R: NULL without a norm before the next block). dX may be dR
+ * itself. Types: dR, R, dX one; B, dH, gates, dB, dGates one. The workspace is needed for
+ * sums only.
+ */
+MAO_API mao_status mao_residual_norm_backward(
+    const mao_mat* dH, const mao_mat* dR, mao_mat B, const mao_mat* R, const float* stats,
+    const mao_row_norm* post, const void* gate, int32_t gate_dtype, const mao_mat* gates,
+    float x_scale, float b_scale, const mao_row_norm* pre, mao_mat dX, mao_mat dB,
+    const mao_mat* dGates, const mao_residual_norm_sums* sums, void* workspace,
+    size_t workspace_bytes, void* stream);
+
+/*
  * Log probabilities of tokens: X holds rows of logits (rows x vocabulary, bf16 or fp32), the
  * results of mao_linear for a model's head. targets: one token (int64) per row; below 0: the
  * row has none (log probability 0, no gradient); at or above the vocabulary's size: NaN. A

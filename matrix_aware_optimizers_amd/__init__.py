@@ -85,6 +85,17 @@ class Adamw8StateC(ctypes.Structure):
                 ("m_out", c_void_p), ("v_out", c_void_p), ("n", c_int64)]
 
 
+class RowNormC(ctypes.Structure):
+    _fields_ = [("kind", c_int32), ("gamma", c_void_p), ("beta", c_void_p),
+                ("param_dtype", c_int32), ("eps", c_float)]
+
+
+class ResidualNormSumsC(ctypes.Structure):
+    _fields_ = [("dpost_gamma", c_void_p), ("dpost_beta", c_void_p), ("dpre_gamma", c_void_p),
+                ("dpre_beta", c_void_p), ("dgate", c_void_p)]
+
+
+ROW_NORMS = {"none": 0, "layer": 1, "rms": 2}
 ADAM_STATES = {"f32": 0, "8bit": 1}
 ADAM_SPAN = 256
 REFRESH_MODES = {"qr": 0, "eigh": 1}
@@ -152,6 +163,15 @@ EXPORTS = {
                                             POINTER(Mat), Mat, c_void_p, c_size_t, c_void_p]),
     "mao_linear_backward_weight": (c_int32, [Mat, POINTER(Mat), POINTER(Q8C), c_int32, Mat,
                                              c_void_p, c_int32, c_void_p, c_size_t, c_void_p]),
+    "mao_residual_norm": (c_int32, [Mat, Mat, POINTER(RowNormC), c_void_p, c_int32, POINTER(Mat),
+                                    c_float, c_float, POINTER(RowNormC), Mat, POINTER(Mat),
+                                    c_void_p, c_void_p]),
+    "mao_residual_norm_backward_workspace_size": (c_size_t, [c_int64, c_int64]),
+    "mao_residual_norm_backward": (c_int32, [POINTER(Mat), POINTER(Mat), Mat, POINTER(Mat), c_void_p,
+                                             POINTER(RowNormC), c_void_p, c_int32, POINTER(Mat),
+                                             c_float, c_float, POINTER(RowNormC), Mat, Mat,
+                                             POINTER(Mat), POINTER(ResidualNormSumsC), c_void_p,
+                                             c_size_t, c_void_p]),
     "mao_token_logprobs": (c_int32, [Mat, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p,
                                      c_void_p, c_void_p]),
     "mao_token_logprobs_backward": (c_int32, [Mat, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
@@ -647,6 +667,46 @@ def linear_backward_weight(dY, X, *, x_act="none", dtype=None, out=None, dbias=N
         raise ValueError("accumulate needs out and dbias")
     return _run("linear_backward_weight", dY, X, _act(x_act), _result_type(dtype, F32), out, dbias,
                 bool(accumulate))
+
+
+def _row_norm(kind):
+    if kind not in ROW_NORMS:
+        raise ValueError(f"unknown norm {kind!r}: one of {', '.join(ROW_NORMS)}")
+    return ROW_NORMS[kind]
+
+
+def residual_norm(X, B, *, gate=None, x_scale=1.0, b_scale=1.0, post="none", post_gamma=None,
+                  post_beta=None, pre="rms", pre_gamma=None, pre_beta=None, eps=1e-5, out=None,
+                  h=None, stats=True):
+    """(R, H, stats) between two blocks: R = x_scale X + b_scale gate * N_post(B), the residual
+    stream X with the block's output B, and H = N_pre(R), the next block's input (None with
+    ``pre="none"``). Norms: "none", "layer" or "rms", with fp32 or bf16 parameters. ``gate``:
+    None, a vector (a gate per channel) or a matrix of B's type. R has X's type, H B's; ``out``
+    may be X. ``stats`` (rows x 4, for the backward call) is None if not wanted."""
+    return _run("residual_norm", X, B, gate, x_scale, b_scale, _row_norm(post), post_gamma, post_beta,
+                _row_norm(pre), pre_gamma, pre_beta, eps, out, h, bool(stats))
+
+
+class ResidualNormGrads(NamedTuple):
+    """Results of residual_norm_backward; None for what the call has not."""
+    dX: object
+    dB: object
+    dgate: object
+    dpost_gamma: object
+    dpost_beta: object
+    dpre_gamma: object
+    dpre_beta: object
+
+
+def residual_norm_backward(dH, dR, B, R, stats, *, gate=None, x_scale=1.0, b_scale=1.0, post="none",
+                           post_gamma=None, post_beta=None, pre="rms", pre_gamma=None, out=None,
+                           sums=True) -> ResidualNormGrads:
+    """The gradients of residual_norm from dH (None with ``pre="none"``, as is R) and dR, the
+    gradient of R from what follows (or None). The other arguments as in the forward call.
+    ``out`` (dX) may be dR. ``sums=False``: no gradients of vectors."""
+    return ResidualNormGrads(*_run("residual_norm_backward", B, dH, dR, R, stats, gate, x_scale,
+                                   b_scale, _row_norm(post), post_gamma, post_beta, _row_norm(pre),
+                                   pre_gamma, out, bool(sums)))
 
 
 class TokenLogprobs(NamedTuple):

@@ -406,6 +406,129 @@ PyObject* linear_backward_weight(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A norm's kind and parameters.
+struct RowNorm {
+  mao_row_norm n;
+  RowNorm(PyObject* kind, PyObject* gamma, PyObject* beta, double eps, int64_t cols, int64_t dev,
+          const char* name) {
+    const Vec g(gamma, cols, dev, name, false), b(beta, cols, dev, name, false);
+    if (g.p && b.p && g.dtype != b.dtype) fail(PyExc_TypeError, "gamma and beta must share a dtype");
+    n = mao_row_norm{(int32_t)integer(kind), g.p, b.p, g.p ? g.dtype : b.dtype, (float)eps};
+  }
+};
+
+// The gate: a vector, a matrix or None.
+struct Gate {
+  void* vec = nullptr;
+  int32_t dtype = MAO_F32;
+  mao_mat m;
+  const mao_mat* mat = nullptr;
+  Gate(PyObject* o, int64_t cols, int64_t dev) {
+    if (o == Py_None) return;
+    if (tensor(o).dim() == 1) {
+      const Vec v(o, cols, dev, "gate", false);
+      vec = v.p;
+      dtype = v.dtype;
+    } else {
+      m = view(tensor(o), dev);
+      mat = &m;
+    }
+  }
+};
+
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Raised{};
+  return v;
+}
+
+// (X, B, gate, x_scale, b_scale, post, post_gamma, post_beta, pre, pre_gamma, pre_beta, eps, out,
+// h, stats, device, stream) -> (R, H, stats)
+PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 17, [&]() -> PyObject* {
+    const int64_t dev = integer(a[15]);
+    const at::Tensor &X = tensor(a[0]), &B = tensor(a[1]);
+    const mao_mat x = view(X, dev), b = view(B, dev);
+    const Gate gate(a[2], b.cols, dev);
+    const double eps = number(a[11]);
+    const RowNorm post(a[5], a[6], a[7], eps, b.cols, dev, "post_gamma or post_beta"),
+        pre(a[8], a[9], a[10], eps, b.cols, dev, "pre_gamma or pre_beta");
+    const at::Tensor r = result(a[12], x.rows, x.cols, X.scalar_type(), X);
+    at::Tensor h, stats;
+    mao_mat hv;
+    const bool normed = pre.n.kind != MAO_ROW_NORM_NONE || a[13] != Py_None;
+    if (normed) {
+      h = result(a[13], b.rows, b.cols, B.scalar_type(), B);
+      hv = view(h, dev);
+    }
+    if (a[14] == Py_True) stats = at::empty({b.rows, 4}, B.options().dtype(at::kFloat));
+    check(mao_residual_norm(x, b, &post.n, gate.vec, gate.dtype, gate.mat, (float)number(a[3]),
+                            (float)number(a[4]), &pre.n, view(r, dev), normed ? &hv : nullptr,
+                            stats.defined() ? (float*)stats.data_ptr() : nullptr,
+                            (void*)integer(a[16])),
+          "mao_residual_norm");
+    return Py_BuildValue("NNN", wrap(r, a[12]), normed ? wrap(h, a[13]) : Py_NewRef(Py_None),
+                         stats.defined() ? THPVariable_Wrap(stats) : Py_NewRef(Py_None));
+  });
+}
+
+// (B, dH, dR, R, stats, gate, x_scale, b_scale, post, post_gamma, post_beta, pre, pre_gamma, out,
+// sums, device, stream) -> (dX, dB, dgate, dpost_gamma, dpost_beta, dpre_gamma, dpre_beta)
+PyObject* residual_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 17, [&]() -> PyObject* {
+    const int64_t dev = integer(a[15]), stream = integer(a[16]);
+    const at::Tensor& B = tensor(a[0]);
+    const mao_mat b = view(B, dev);
+    const Opt dh(a[1], dev), dr(a[2], dev), r(a[3], dev);
+    const at::Tensor& st = tensor(a[4]);
+    if (st.scalar_type() != at::kFloat) fail(PyExc_TypeError, "stats must be float32");
+    if (st.dim() != 2 || st.size(0) != b.rows || st.size(1) != 4 || !st.is_contiguous())
+      fail(PyExc_ValueError, "stats must be the forward pass's (rows x 4)");
+    on_device(st, dev);
+    const Gate gate(a[5], b.cols, dev);
+    // eps has gone into the statistics
+    const RowNorm post(a[8], a[9], a[10], 1.0, b.cols, dev, "post_gamma or post_beta"),
+        pre(a[11], a[12], Py_None, 1.0, b.cols, dev, "pre_gamma");
+    if (!dr.p && !r.p) fail(PyExc_ValueError, "dH (with R) or dR is needed");
+    const at::Tensor& stream_like = tensor(r.p ? a[3] : a[2]);
+    const at::Tensor dx = result(a[13], b.rows, b.cols, stream_like.scalar_type(), B);
+    const at::Tensor db = result(Py_None, b.rows, b.cols, B.scalar_type(), B);
+    at::Tensor dgates, vecs[5];
+    mao_mat dgv;
+    if (gate.mat) {
+      dgates = result(Py_None, b.rows, b.cols, B.scalar_type(), B);
+      dgv = view(dgates, dev);
+    }
+    float* p[5] = {};
+    if (a[14] == Py_True) {
+      const bool want[5] = {post.n.kind != MAO_ROW_NORM_NONE, post.n.kind == MAO_ROW_NORM_LAYER,
+                            pre.n.kind != MAO_ROW_NORM_NONE, pre.n.kind == MAO_ROW_NORM_LAYER,
+                            gate.vec != nullptr};
+      for (int k = 0; k < 5; ++k)
+        if (want[k]) {
+          vecs[k] = at::empty({b.cols}, B.options().dtype(at::kFloat));
+          p[k] = (float*)vecs[k].data_ptr();
+        }
+    }
+    const mao_residual_norm_sums sums{p[0], p[1], p[2], p[3], p[4]};
+    const bool any = p[0] || p[1] || p[2] || p[3] || p[4];
+    const Workspace ws(any ? mao_residual_norm_backward_workspace_size(b.rows, b.cols) : 0, dev,
+                       stream);
+    check(mao_residual_norm_backward(dh.p, dr.p, b, r.p, (const float*)st.data_ptr(), &post.n,
+                                     gate.vec, gate.dtype, gate.mat, (float)number(a[6]),
+                                     (float)number(a[7]), &pre.n, view(dx, dev), view(db, dev),
+                                     gate.mat ? &dgv : nullptr, &sums, ws.p, ws.bytes,
+                                     (void*)stream),
+          "mao_residual_norm_backward");
+    const auto out = [](const at::Tensor& t) {
+      return t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None);
+    };
+    return Py_BuildValue("NNNNNNN", wrap(dx, a[13]), THPVariable_Wrap(db),
+                         gate.mat ? THPVariable_Wrap(dgates) : out(vecs[4]), out(vecs[0]),
+                         out(vecs[1]), out(vecs[2]), out(vecs[3]));
+  });
+}
+
 // One token per row.
 const int64_t* tokens_of(PyObject* o, int64_t rows, int64_t dev) {
   if (o == Py_None) return nullptr;
@@ -547,15 +670,10 @@ struct Numbers {
                      (long long)q.size(), (long long)n);
         throw Raised{};
       }
-      for (int64_t i = 0; i < n; ++i) each.push_back(number(q[i]));
+      for (int64_t i = 0; i < n; ++i) each.push_back((float)number(q[i]));
     } else {
-      one = number(o);
+      one = (float)number(o);
     }
-  }
-  static float number(PyObject* o) {
-    const double v = PyFloat_AsDouble(o);
-    if (v == -1.0 && PyErr_Occurred()) throw Raised{};
-    return (float)v;
   }
   float operator[](int64_t i) const { return each.empty() ? one : each[(size_t)i]; }
 };
@@ -598,7 +716,7 @@ PyObject* adamw_step_many(PyObject*, PyObject* const* a, Py_ssize_t n) {
       gs = (const float*)f.p;
     }
     check(adamw_step_many((int32_t)std::min<int64_t>(count, INT32_MAX), t.data(), integer(a[2]),
-                          Numbers::number(a[4]), Numbers::number(a[5]), Numbers::number(a[6]), gs,
+                          (float)number(a[4]), (float)number(a[5]), (float)number(a[6]), gs,
                           (void*)integer(a[10])),
           "adamw_step_many");
     Py_RETURN_NONE;
@@ -673,6 +791,8 @@ PyMethodDef g_methods[] = {MAO_METHOD(init),
                            MAO_METHOD(linear),
                            MAO_METHOD(linear_backward_input),
                            MAO_METHOD(linear_backward_weight),
+                           MAO_METHOD(residual_norm),
+                           MAO_METHOD(residual_norm_backward),
                            MAO_METHOD(token_logprobs),
                            MAO_METHOD(token_logprobs_backward),
                            MAO_METHOD(token_loss),

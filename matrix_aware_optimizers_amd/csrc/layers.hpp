@@ -218,4 +218,42 @@ struct TokenBackArgs {
 mao_status launch_tokens_backward(const TokenBackArgs& a, int dtype, hipStream_t s);
 mao_status launch_token_loss(const TokenBackArgs& a, int dtype, hipStream_t s);
 
+// ---- between two blocks (residual_norm.hip) --------------------------------
+constexpr int64_t kJoinMaxCols = 16384;
+
+struct JoinNorm {
+  const void *gamma, *beta;  // or nullptr (1, 0)
+  int kind, p_dtype;         // mao_row_norm_kind
+  float eps;
+};
+struct JoinArgs {
+  const void *x, *b;
+  const void* gate;      // per element, or nullptr
+  const void* gate_vec;  // per column, or nullptr
+  void *r, *h;           // h: nullptr without a norm after the sum
+  float* stats;          // (mean, rstd) of both norms per row, or nullptr
+  int64_t ldx, ldb, ldgate, ldr, ldh;
+  int rows, cols, gate_dtype;
+  float xs, bs;
+  JoinNorm post, pre;
+};
+mao_status launch_join(const JoinArgs& a, int stream_type, int block_type, hipStream_t s);
+
+struct JoinBackArgs {
+  const void *dh, *dr;  // or nullptr
+  const void *b, *r;    // r: nullptr without a norm after the sum
+  const float* stats;
+  const void *gate, *gate_vec;
+  void *dx, *db, *dgate;  // dgate: per element, or nullptr
+  float *dpost_gamma, *dpost_beta, *dpre_gamma, *dpre_beta, *dgate_vec;  // or nullptr
+  float* part;  // [blocks][4][cols], or nullptr
+  int64_t lddh, lddr, ldb, ldr, ldgate, lddx, lddb, lddgate;
+  int rows, cols, gate_dtype;
+  float xs, bs;
+  JoinNorm post, pre;
+};
+int join_blocks(int64_t rows, int64_t cols);
+mao_status launch_join_backward(const JoinBackArgs& a, int stream_type, int block_type,
+                                hipStream_t s);
+
 }  // namespace mao

@@ -62,7 +62,7 @@ bool same_view(const mao_mat& a, const mao_mat& b) {
 // The buffers of one call, outputs first: no output may share bytes with any
 // other buffer.
 struct Buffers {
-  Range r[16];
+  Range r[24];
   int n = 0, outs = 0;
   void out(Range x) {
     r[n++] = x;
@@ -108,6 +108,51 @@ WeightWs carve_weight(void* base, int64_t rows, int64_t k, int64_t n, int dtype,
   w.sums = c.take<float>((size_t)lin_sum_rows(dtype, n, k, rows) * n);
   w.bytes = c.used;
   return w;
+}
+
+mao_status check_row_norm(const char* name, const mao_row_norm* n) {
+  if (!n) MAO_FAIL(MAO_E_NULL, "%s is NULL", name);
+  if (n->kind < MAO_ROW_NORM_NONE || n->kind > MAO_ROW_NORM_RMS) MAO_FAIL(MAO_E_HPARAM, "%s: kind=%d", name, n->kind);
+  if ((n->kind == MAO_ROW_NORM_NONE && n->gamma) || (n->kind != MAO_ROW_NORM_LAYER && n->beta))
+    MAO_FAIL(MAO_E_HPARAM, "%s: parameters that this kind of norm has not", name);
+  MAO_TRY(check_vector(name, n->gamma, n->param_dtype));
+  MAO_TRY(check_vector(name, n->beta, n->param_dtype));
+  if (n->kind != MAO_ROW_NORM_NONE && (!finite(n->eps) || n->eps <= 0.f))
+    MAO_FAIL(MAO_E_HPARAM, "%s: eps=%g must be > 0", name, (double)n->eps);
+  return MAO_OK;
+}
+JoinNorm norm_of(const mao_row_norm& n) {
+  return {n.gamma, n.beta, n.kind, n.param_dtype, n.eps};
+}
+// What both directions of the join share.
+mao_status check_join(const mao_mat& B, const mao_row_norm* post, const void* gate, int gate_dtype,
+                      const mao_mat* gates, float x_scale, float b_scale, const mao_row_norm* pre) {
+  MAO_TRY(check_view("B", B));
+  if (B.cols > kJoinMaxCols) MAO_FAIL(MAO_E_UNSUPPORTED, "cols=%lld above %lld", (long long)B.cols, (long long)kJoinMaxCols);
+  MAO_TRY(check_row_norm("post", post));
+  MAO_TRY(check_row_norm("pre", pre));
+  if (gate && gates) MAO_FAIL(MAO_E_NULL, "at most one of gate and gates");
+  MAO_TRY(check_vector("gate", gate, gate_dtype));
+  if (gates) MAO_TRY(check_shape("gates", *gates, B.rows, B.cols));
+  if (gates && gates->dtype != B.dtype) MAO_FAIL(MAO_E_DTYPE, "B and gates must share a dtype");
+  if (!finite(x_scale) || !finite(b_scale)) MAO_FAIL(MAO_E_HPARAM, "x_scale=%g b_scale=%g", (double)x_scale, (double)b_scale);
+  return MAO_OK;
+}
+mao_status check_typed(const char* name, const mao_mat& m, const mao_mat& like, int dtype) {
+  MAO_TRY(check_shape(name, m, like.rows, like.cols));
+  if (m.dtype != dtype) MAO_FAIL(MAO_E_DTYPE, "%s: dtype %d, expected %d", name, m.dtype, dtype);
+  return MAO_OK;
+}
+void add_join_inputs(Buffers& b, const mao_mat& B, const mao_row_norm* post, const void* gate,
+                     int gate_dtype, const mao_mat* gates, const mao_row_norm* pre) {
+  b.in(range_of(B));
+  for (const mao_row_norm* n : {post, pre}) {
+    const int64_t bytes = B.cols * (int64_t)dtype_size(n->param_dtype);
+    if (n->gamma) b.in(range_of(n->gamma, bytes));
+    if (n->beta) b.in(range_of(n->beta, bytes));
+  }
+  if (gate) b.in(range_of(gate, B.cols * (int64_t)dtype_size(gate_dtype)));
+  if (gates) b.in(range_of(*gates));
 }
 
 constexpr int64_t kMostBlocks = (1 << 24) - 1;  // of 256 threads: a launch has below 2^32
@@ -475,6 +520,147 @@ mao_status mao_linear_backward_weight(mao_mat dY, const mao_mat* X, const mao_q8
     MAO_TRY(launch_partial_sum(w.sums, p.M, lin_sum_rows(dY.dtype, p.M, p.N, p.K), p.M, dbias,
                                nullptr, 0, accumulate != 0, s));
   return MAO_OK;
+}
+
+mao_status mao_residual_norm(mao_mat X, mao_mat B, const mao_row_norm* post, const void* gate,
+                             int32_t gate_dtype, const mao_mat* gates, float x_scale,
+                             float b_scale, const mao_row_norm* pre, mao_mat R, const mao_mat* H,
+                             float* stats, void* stream) {
+  MAO_TRY(check_join(B, post, gate, gate_dtype, gates, x_scale, b_scale, pre));
+  MAO_TRY(check_shape("X", X, B.rows, B.cols));
+  MAO_TRY(check_typed("R", R, B, X.dtype));
+  if ((H != nullptr) != (pre->kind != MAO_ROW_NORM_NONE)) MAO_FAIL(MAO_E_NULL, "H goes with a norm before the next block");
+  if (H) MAO_TRY(check_typed("H", *H, B, B.dtype));
+  if ((uintptr_t)stats % 16 != 0) MAO_FAIL(MAO_E_LAYOUT, "stats not 16-byte aligned");
+  Buffers b;
+  b.out(range_of(R));
+  if (H) b.out(range_of(*H));
+  if (stats) b.out(range_of(stats, B.rows * 16));
+  if (!same_view(X, R)) b.in(range_of(X));
+  add_join_inputs(b, B, post, gate, gate_dtype, gates, pre);
+  MAO_TRY(b.check());
+  JoinArgs a = {};
+  a.x = X.data;
+  a.ldx = X.ld;
+  a.b = B.data;
+  a.ldb = B.ld;
+  a.gate_vec = gate;
+  a.gate_dtype = gate_dtype;
+  if (gates) {
+    a.gate = gates->data;
+    a.ldgate = gates->ld;
+  }
+  a.r = R.data;
+  a.ldr = R.ld;
+  if (H) {
+    a.h = H->data;
+    a.ldh = H->ld;
+  }
+  a.stats = stats;
+  a.rows = (int)B.rows;
+  a.cols = (int)B.cols;
+  a.xs = x_scale;
+  a.bs = b_scale;
+  a.post = norm_of(*post);
+  a.pre = norm_of(*pre);
+  return launch_join(a, X.dtype, B.dtype, (hipStream_t)stream);
+}
+
+size_t mao_residual_norm_backward_workspace_size(int64_t rows, int64_t cols) {
+  if (!sizes_ok(rows, cols, 1) || cols > kJoinMaxCols) return 0;
+  return (size_t)join_blocks(rows, cols) * 4 * cols * 4;
+}
+
+mao_status mao_residual_norm_backward(const mao_mat* dH, const mao_mat* dR, mao_mat B,
+                                      const mao_mat* R, const float* stats,
+                                      const mao_row_norm* post, const void* gate,
+                                      int32_t gate_dtype, const mao_mat* gates, float x_scale,
+                                      float b_scale, const mao_row_norm* pre, mao_mat dX,
+                                      mao_mat dB, const mao_mat* dGates,
+                                      const mao_residual_norm_sums* sums, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+  MAO_TRY(check_join(B, post, gate, gate_dtype, gates, x_scale, b_scale, pre));
+  const bool normed = pre->kind != MAO_ROW_NORM_NONE;
+  MAO_TRY(check_shape("dX", dX, B.rows, B.cols));
+  MAO_TRY(check_typed("dB", dB, B, B.dtype));
+  if ((dH != nullptr) != normed || (R != nullptr) != normed)
+    MAO_FAIL(MAO_E_NULL, "dH and R go with a norm before the next block");
+  if (!dH && !dR) MAO_FAIL(MAO_E_NULL, "no gradient is given");
+  if (dH) MAO_TRY(check_typed("dH", *dH, B, B.dtype));
+  if (R) MAO_TRY(check_typed("R", *R, B, dX.dtype));
+  if (dR) MAO_TRY(check_typed("dR", *dR, B, dX.dtype));
+  if (dGates && !gates) MAO_FAIL(MAO_E_NULL, "dGates without gates");
+  if (dGates) MAO_TRY(check_typed("dGates", *dGates, B, B.dtype));
+  if (!stats) MAO_FAIL(MAO_E_NULL, "stats is NULL");
+  if ((uintptr_t)stats % 16 != 0) MAO_FAIL(MAO_E_LAYOUT, "stats not 16-byte aligned");
+  mao_residual_norm_sums v = {};
+  if (sums) v = *sums;
+  float* const vecs[] = {v.dpost_gamma, v.dpost_beta, v.dpre_gamma, v.dpre_beta, v.dgate};
+  bool any = false;
+  for (float* p : vecs) {
+    MAO_TRY(check_floats("vector gradient", p));
+    any = any || p;
+  }
+  if ((v.dpost_gamma && post->kind == MAO_ROW_NORM_NONE) || (v.dpre_gamma && !normed) ||
+      (v.dpost_beta && post->kind != MAO_ROW_NORM_LAYER) || (v.dpre_beta && pre->kind != MAO_ROW_NORM_LAYER) ||
+      (v.dgate && !gate))
+    MAO_FAIL(MAO_E_HPARAM, "the gradient of a parameter that the call has not");
+  const size_t need = any ? mao_residual_norm_backward_workspace_size(B.rows, B.cols) : 0;
+  MAO_TRY(check_workspace(workspace, workspace_bytes, need));
+  Buffers b;
+  b.out(range_of(dX));
+  b.out(range_of(dB));
+  if (dGates) b.out(range_of(*dGates));
+  for (float* p : vecs)
+    if (p) b.out(range_of(p, B.cols * 4));
+  if (need) b.out(range_of(workspace, (int64_t)need));
+  add_join_inputs(b, B, post, gate, gate_dtype, gates, pre);
+  if (dH) b.in(range_of(*dH));
+  if (R) b.in(range_of(*R));
+  if (dR && !same_view(*dR, dX)) b.in(range_of(*dR));
+  b.in(range_of(stats, B.rows * 16));
+  MAO_TRY(b.check());
+  JoinBackArgs a = {};
+  if (dH) {
+    a.dh = dH->data;
+    a.lddh = dH->ld;
+    a.r = R->data;
+    a.ldr = R->ld;
+  }
+  if (dR) {
+    a.dr = dR->data;
+    a.lddr = dR->ld;
+  }
+  a.b = B.data;
+  a.ldb = B.ld;
+  a.stats = stats;
+  a.gate_vec = gate;
+  a.gate_dtype = gate_dtype;
+  if (gates) {
+    a.gate = gates->data;
+    a.ldgate = gates->ld;
+  }
+  a.dx = dX.data;
+  a.lddx = dX.ld;
+  a.db = dB.data;
+  a.lddb = dB.ld;
+  if (dGates) {
+    a.dgate = dGates->data;
+    a.lddgate = dGates->ld;
+  }
+  a.dpost_gamma = v.dpost_gamma;
+  a.dpost_beta = v.dpost_beta;
+  a.dpre_gamma = v.dpre_gamma;
+  a.dpre_beta = v.dpre_beta;
+  a.dgate_vec = v.dgate;
+  a.part = any ? (float*)workspace : nullptr;
+  a.rows = (int)B.rows;
+  a.cols = (int)B.cols;
+  a.xs = x_scale;
+  a.bs = b_scale;
+  a.post = norm_of(*post);
+  a.pre = norm_of(*pre);
+  return launch_join_backward(a, dX.dtype, B.dtype, (hipStream_t)stream);
 }
 
 mao_status mao_token_logprobs(mao_mat X, const int64_t* targets, float* logprob, float* entropy,

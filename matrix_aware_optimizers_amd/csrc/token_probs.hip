@@ -406,17 +406,6 @@ __global__ __launch_bounds__(THREADS) void token_kernel(TokenArgs a) {
   if (threadIdx.x == 0) write_row<T>(a, row, q);
 }
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-// A row for buffer instructions: past its `bytes` they read 0 and write nothing. One offset
-// register serves every access of a thread (64-bit addresses of the pieces of two rows took 93
-// registers where 64 let two workgroups share a CU).
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const void* p, int64_t row_bytes,
-                                                             int row, int bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc((char*)p + row_bytes * row, 0, bytes, 0x00027000);
-}
-
 // Gradients work on pieces of 16 bytes: consecutive lanes read consecutive ones. (fp32 in
 // runs of 8, of which each load takes every other 16 bytes: 2045 x 50301 167 us for 145.)
 template <typename T> struct Piece {
