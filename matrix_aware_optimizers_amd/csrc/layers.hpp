@@ -252,7 +252,7 @@ struct JoinBackArgs {
   float xs, bs;
   JoinNorm post, pre;
 };
-int join_blocks(int64_t rows, int64_t cols);
+int join_blocks(bool all_bf16, int64_t rows, int64_t cols);
 mao_status launch_join_backward(const JoinBackArgs& a, int stream_type, int block_type,
                                 hipStream_t s);
 

@@ -3,6 +3,8 @@
 #include "layers.hpp"
 #include "validate.hpp"
 
+#include <algorithm>
+
 namespace mao {
 
 namespace {
@@ -568,7 +570,8 @@ mao_status mao_residual_norm(mao_mat X, mao_mat B, const mao_row_norm* post, con
 
 size_t mao_residual_norm_backward_workspace_size(int64_t rows, int64_t cols) {
   if (!sizes_ok(rows, cols, 1) || cols > kJoinMaxCols) return 0;
-  return (size_t)join_blocks(rows, cols) * 4 * cols * 4;
+  // the types that take more partial rows
+  return (size_t)std::max(join_blocks(true, rows, cols), join_blocks(false, rows, cols)) * 4 * cols * 4;
 }
 
 mao_status mao_residual_norm_backward(const mao_mat* dH, const mao_mat* dR, mao_mat B,

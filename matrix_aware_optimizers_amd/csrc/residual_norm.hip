@@ -30,30 +30,93 @@ namespace mao {
 
 namespace {
 
-template <typename TX, typename TB, int TPR, int V>
-__global__ __launch_bounds__(TPR) void join_fwd_kernel(JoinArgs a) {
-  __shared__ float red[2][4][TPR / 64];
-  int t = threadIdx.x;
+// Results that would push everything else out of the L2s (32 MB) go past them.
+__device__ __forceinline__ bool past_l2(int rows, int cols) {
+  return (int64_t)rows * cols >= (int64_t)1 << 23;
+}
+
+// Parameter vectors of a workgroup in LDS, as fp32 (LDS: up to 4096 columns forward, 8192
+// backward; rows of a CU read them from there instead of holding 5 values a column in
+// registers), or read where they are.
+struct Vector {
+  const void* p;  // or nullptr: dflt
+  int dtype;
+  float dflt;
+};
+template <int N, int COLS, int BLK>
+__device__ __forceinline__ void stage(const Vector (&from)[N], int cols, float (*to)[COLS]) {
+  constexpr int K = (COLS + BLK - 1) / BLK;
+  uint32_t raw[N][K];
+  // all loads first, conversions after
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (int)threadIdx.x + k * BLK;
+      raw[n][k] = 0;
+      if (from[n].p && c < cols)
+        raw[n][k] = from[n].dtype == MAO_BF16 ? ((const bf16_t*)from[n].p)[c]
+                                              : ((const uint32_t*)from[n].p)[c];
+    }
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (int)threadIdx.x + k * BLK;
+      const uint32_t u = from[n].dtype == MAO_BF16 ? raw[n][k] << 16 : raw[n][k];
+      if (c < COLS) to[n][c] = from[n].p ? __uint_as_float(u) : from[n].dflt;
+    }
+}
+// Where a kernel has its vectors: a thread with one run of columns keeps their values.
+enum { kInRegisters, kInLds, kInMemory };
+constexpr int vectors_at(int v, bool lds) { return v == 1 ? kInRegisters : lds ? kInLds : kInMemory; }
+
+template <bool LDS>
+__device__ __forceinline__ void vector4(const Vector& from, const float* staged, int run, int cols,
+                                        float (&v)[4]) {
+  if constexpr (LDS) {
+    const float4 k = *(const float4*)(staged + 4 * run);
+    v[0] = k.x;
+    v[1] = k.y;
+    v[2] = k.z;
+    v[3] = k.w;
+  } else {
+    load_param4(from.p, from.dtype, 4 * run, cols - 4 * run, from.dflt, v);
+  }
+}
+
+template <typename TX, typename TB, int TPR, int V, int BLK, bool LDS>
+__global__ __launch_bounds__(BLK) void join_fwd_kernel(JoinArgs a) {
+  constexpr int RPB = BLK / TPR, COLS = 4 * TPR * V;
+  __shared__ float red[2][4][BLK / 64];
+  constexpr bool STAGED = vectors_at(V, LDS) == kInLds;
+  __shared__ float vecs[STAGED ? 5 : 1][STAGED ? COLS : 1];
+  // a wavefront has one row
+  const int sub = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
+  int t = threadIdx.x % TPR;
   const float inv_n = 1.f / (float)a.cols;
-  constexpr bool PRE = V == 1;  // parameters stay in registers
-  constexpr int P = PRE ? V : 1;
-  float g1[P][4], b1[P][4], g2[P][4], b2[P][4], gate[P][4];
-  auto params = [&](int v, int i) __attribute__((always_inline)) {
-    const int col = 4 * (t + v * TPR), valid = a.cols - col;
-    load_param4(a.post.gamma, a.post.p_dtype, col, valid, 1.f, g1[i]);
-    load_param4(a.post.beta, a.post.p_dtype, col, valid, 0.f, b1[i]);
-    load_param4(a.pre.gamma, a.pre.p_dtype, col, valid, 1.f, g2[i]);
-    load_param4(a.pre.beta, a.pre.p_dtype, col, valid, 0.f, b2[i]);
-    load_param4(a.gate_vec, a.gate_dtype, col, valid, 1.f, gate[i]);
+  const bool past = past_l2(a.rows, a.cols);
+  const Vector from[5] = {{a.post.gamma, a.post.p_dtype, 1.f}, {a.post.beta, a.post.p_dtype, 0.f},
+                          {a.gate_vec, a.gate_dtype, 1.f}, {a.pre.gamma, a.pre.p_dtype, 1.f},
+                          {a.pre.beta, a.pre.p_dtype, 0.f}};
+  constexpr int AT = vectors_at(V, LDS);
+  float held[AT == kInRegisters ? 5 : 1][4];
+  auto vec = [&](int n, int v, float (&w)[4]) __attribute__((always_inline)) {
+    if constexpr (AT == kInRegisters) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = held[AT == kInRegisters ? n : 0][i];
+    } else {
+      vector4<AT == kInLds>(from[n], vecs[AT == kInLds ? n : 0], t + v * TPR, a.cols, w);
+    }
   };
-  if constexpr (PRE) params(0, 0);
   Run4<TX> rx[V];
   Run4<TB> rb[V], rg[V];
   const int xbytes = run4_bytes<TX>(a.cols), bbytes = run4_bytes<TB>(a.cols);
   auto fetch = [&](int row) __attribute__((always_inline)) {
-    const auto x = row_buffer(a.x, a.ldx * (int64_t)sizeof(TX), row, xbytes);
-    const auto b = row_buffer(a.b, a.ldb * (int64_t)sizeof(TB), row, bbytes);
-    const auto g = row_buffer(a.gate, a.ldgate * (int64_t)sizeof(TB), row, a.gate ? bbytes : 0);
+    const bool live = row < a.rows;
+    const auto x = row_buffer(a.x, a.ldx * (int64_t)sizeof(TX), row, live ? xbytes : 0);
+    const auto b = row_buffer(a.b, a.ldb * (int64_t)sizeof(TB), row, live ? bbytes : 0);
+    const auto g = row_buffer(a.gate, a.ldgate * (int64_t)sizeof(TB), row, live && a.gate ? bbytes : 0);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       rx[v].load(x, t + v * TPR);
@@ -61,11 +124,23 @@ __global__ __launch_bounds__(TPR) void join_fwd_kernel(JoinArgs a) {
       if (a.gate) rg[v].load(g, t + v * TPR);
     }
   };
-  int row = blockIdx.x, turn = 0;
-  fetch(row);
-  for (; row < a.rows; row += gridDim.x, turn ^= 1) {
-    // columns and parameters of several runs anew for each row: kept over the rows they spill
+  const int step = gridDim.x * RPB;
+  int r0 = blockIdx.x * RPB, turn = 0;
+  fetch(r0 + sub);
+  if constexpr (AT == kInLds) {
+    stage<5, COLS, BLK>(from, a.cols, vecs);
+    __syncthreads();
+  }
+  if constexpr (AT == kInRegisters) {
+#pragma unroll
+    for (int n = 0; n < 5; ++n) vector4<false>(from[n], nullptr, t, a.cols, held[n]);
+  }
+  // every thread of the block runs the same number of rounds (barriers inside)
+  for (; r0 < a.rows; r0 += step, turn ^= 1) {
+    // columns anew for each row: kept over the rows they spill
     if (V > 1) asm volatile("" : "+v"(t));
+    const int row = r0 + sub;
+    const bool live = row < a.rows;
     float x[V][4], u[V][4], g[V][4];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -77,7 +152,7 @@ __global__ __launch_bounds__(TPR) void join_fwd_kernel(JoinArgs a) {
       mask4(x[v], valid);
       mask4(u[v], valid);
     }
-    if (row + (int)gridDim.x < a.rows) fetch(row + (int)gridDim.x);
+    if (r0 + step < a.rows) fetch(row + step);
     // z <- its deviations from the mean; (mean, rstd). Only the two sums depend on the kind.
     auto moments = [&](float (&z)[V][4], const JoinNorm& k, float* buf0, float* buf1, float& mean,
                        float& rstd) __attribute__((always_inline)) {
@@ -108,57 +183,61 @@ __global__ __launch_bounds__(TPR) void join_fwd_kernel(JoinArgs a) {
     moments(u, a.post, red[turn][0], red[turn][1], m1, r1);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = t + v * TPR, valid = a.cols - 4 * c, i0 = PRE ? v : 0;
-      if constexpr (!PRE) params(v, 0);
+      const int c = t + v * TPR, valid = a.cols - 4 * c;
+      float g1[4], b1[4], gate[4];
+      vec(0, v, g1);
+      vec(1, v, b1);
+      vec(2, v, gate);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float w = u[v][i] * r1 * g1[i0][i] + b1[i0][i];
-        w *= a.gate ? g[v][i] : gate[i0][i];
+        const float w = (u[v][i] * r1 * g1[i] + b1[i]) * (a.gate ? g[v][i] : gate[i]);
         x[v][i] = a.xs * x[v][i] + a.bs * w;
       }
       mask4(x[v], valid);
-      store_run4<TX>(a.r, a.ldr, row, a.cols, c, x[v]);
+      if (live) store_run4<TX>(a.r, a.ldr, row, a.cols, c, x[v], past);
     }
     moments(x, a.pre, red[turn][2], red[turn][3], m2, r2);
+    if (!live) continue;
     if (a.h) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int c = t + v * TPR, i0 = PRE ? v : 0;
-        if constexpr (!PRE) params(v, 0);
-        float y[4];
+        float g2[4], b2[4], y[4];
+        vec(3, v, g2);
+        vec(4, v, b2);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = x[v][i] * r2 * g2[i0][i] + b2[i0][i];
-        store_run4<TB>(a.h, a.ldh, row, a.cols, c, y);
+        for (int i = 0; i < 4; ++i) y[i] = x[v][i] * r2 * g2[i] + b2[i];
+        store_run4<TB>(a.h, a.ldh, row, a.cols, t + v * TPR, y, past);
       }
     }
     if (t == 0 && a.stats) *(float4*)(a.stats + 4 * (int64_t)row) = make_float4(m1, r1, m2, r2);
   }
 }
 
-template <typename TX, typename TB, int TPR, int V, int BLK>
+template <typename TX, typename TB, int TPR, int V, int BLK, bool LDS>
 __global__ __launch_bounds__(BLK) void join_bwd_kernel(JoinBackArgs a) {
-  constexpr int RPB = BLK / TPR;
-  constexpr int kJoin = RPB > 1 ? 4 * V * TPR : 1;
+  constexpr int RPB = BLK / TPR, COLS = 4 * TPR * V;
   __shared__ float2 red[2][2][BLK / 64];
-  __shared__ float join[kJoin];
+  // parameters (the last one: the gate of each channel, or with gates of their own beta1); at
+  // the end the joining of the column sums
+  constexpr int AT = vectors_at(V, LDS);
+  __shared__ float vecs[AT == kInLds ? 3 : 1][AT == kInLds || RPB > 1 ? COLS : 1];
   // a wavefront has one row
   int t = threadIdx.x % TPR;
   const int sub = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
   const float inv_n = 1.f / (float)a.cols;
-  constexpr bool PRE = V == 1;  // parameters stay in registers
-  constexpr int P = PRE ? V : 1;
-  // the last one: the gate of each channel, or with gates of their own beta1
-  float g1[P][4], g2[P][4], last[P][4];
-  auto params = [&](int v, int i) __attribute__((always_inline)) {
-    const int col = 4 * (t + v * TPR), valid = a.cols - col;
-    load_param4(a.post.gamma, a.post.p_dtype, col, valid, 1.f, g1[i]);
-    load_param4(a.pre.gamma, a.pre.p_dtype, col, valid, 1.f, g2[i]);
-    if (a.gate)
-      load_param4(a.post.beta, a.post.p_dtype, col, valid, 0.f, last[i]);
-    else
-      load_param4(a.gate_vec, a.gate_dtype, col, valid, 1.f, last[i]);
+  const bool past = past_l2(a.rows, a.cols);
+  const Vector from[3] = {{a.post.gamma, a.post.p_dtype, 1.f}, {a.pre.gamma, a.pre.p_dtype, 1.f},
+                          {a.gate ? a.post.beta : a.gate_vec, a.gate ? a.post.p_dtype : a.gate_dtype,
+                           a.gate ? 0.f : 1.f}};
+  float held[AT == kInRegisters ? 3 : 1][4];
+  auto vec = [&](int n, int v, float (&w)[4]) __attribute__((always_inline)) {
+    if constexpr (AT == kInRegisters) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = held[AT == kInRegisters ? n : 0][i];
+    } else {
+      vector4<AT == kInLds>(from[n], vecs[AT == kInLds ? n : 0], t + v * TPR, a.cols, w);
+    }
   };
-  if constexpr (PRE) params(0, 0);
   float sums[4][V][4];  // A, D, dgamma2, dbeta2
 #pragma unroll
   for (int k = 0; k < 4; ++k)
@@ -169,56 +248,80 @@ __global__ __launch_bounds__(BLK) void join_bwd_kernel(JoinBackArgs a) {
   const bool pre = a.pre.kind != MAO_ROW_NORM_NONE, post = a.post.kind != MAO_ROW_NORM_NONE;
   const float pre_mean = a.pre.kind == MAO_ROW_NORM_LAYER ? inv_n : 0.f;
   const float post_mean = a.post.kind == MAO_ROW_NORM_LAYER ? inv_n : 0.f;
-  struct Row {
-    Run4<TX> d[V], r[V];
-    Run4<TB> dh[V], b[V], g[V];
-    float4 st;
-  };
+  // One row in its stored form; a run of the next row is on its way as soon as this row's has
+  // been used for the last time. (KEEP; else no registers are left for it, and each run is
+  // loaded, from the cache after the first time, where it is used.)
+  constexpr bool KEEP = V <= 2;
+  constexpr int Q = KEEP ? V : 1;
+  Run4<TX> qd[Q], qr[Q];
+  Run4<TB> qh[Q], qb[Q], qg[Q];
+  float4 st, next_st;
   const int xbytes = run4_bytes<TX>(a.cols), bbytes = run4_bytes<TB>(a.cols);
-  auto fetch = [&](Row& q, int row) __attribute__((always_inline)) {
+  struct Bufs {
+    __amdgpu_buffer_rsrc_t d, r, dh, b, g;
+  };
+  auto buffers = [&](int row) __attribute__((always_inline)) {
+    return Bufs{row_buffer(a.dr, a.lddr * (int64_t)sizeof(TX), row, a.dr ? xbytes : 0),
+                row_buffer(a.r, a.ldr * (int64_t)sizeof(TX), row, pre ? xbytes : 0),
+                row_buffer(a.dh, a.lddh * (int64_t)sizeof(TB), row, pre ? bbytes : 0),
+                row_buffer(a.b, a.ldb * (int64_t)sizeof(TB), row, bbytes),
+                row_buffer(a.gate, a.ldgate * (int64_t)sizeof(TB), row, a.gate ? bbytes : 0)};
+  };
+  auto fetch = [&](int row) __attribute__((always_inline)) {  // all but b
     row = min(row, a.rows - 1);
-    q.st = *(const float4*)(a.stats + 4 * (int64_t)row);
-    const auto d = row_buffer(a.dr, a.lddr * (int64_t)sizeof(TX), row, a.dr ? xbytes : 0);
-    const auto r = row_buffer(a.r, a.ldr * (int64_t)sizeof(TX), row, pre ? xbytes : 0);
-    const auto dh = row_buffer(a.dh, a.lddh * (int64_t)sizeof(TB), row, pre ? bbytes : 0);
-    const auto b = row_buffer(a.b, a.ldb * (int64_t)sizeof(TB), row, bbytes);
-    const auto g = row_buffer(a.gate, a.ldgate * (int64_t)sizeof(TB), row, a.gate ? bbytes : 0);
+    next_st = *(const float4*)(a.stats + 4 * (int64_t)row);
+    if constexpr (KEEP) {
+      const Bufs f = buffers(row);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = t + v * TPR;
-      q.dh[v].load(dh, c);
-      q.r[v].load(r, c);
-      q.d[v].load(d, c);
-      q.b[v].load(b, c);
-      if (a.gate) q.g[v].load(g, c);
+      for (int v = 0; v < V; ++v) {
+        qh[v].load(f.dh, t + v * TPR);
+        qr[v].load(f.r, t + v * TPR);
+        qd[v].load(f.d, t + v * TPR);
+        if (a.gate) qg[v].load(f.g, t + v * TPR);
+      }
     }
   };
-  auto handle = [&](Row& q, int row, float2 (*buf)[BLK / 64]) __attribute__((always_inline)) {
+  auto fetch_b = [&](int row) __attribute__((always_inline)) {
+    if constexpr (KEEP) {
+      const Bufs f = buffers(min(row, a.rows - 1));
+#pragma unroll
+      for (int v = 0; v < V; ++v) qb[v].load(f.b, t + v * TPR);
+    }
+  };
+  auto handle = [&](int row, int next, float2 (*buf)[BLK / 64]) __attribute__((always_inline)) {
+    if (V > 1) asm volatile("" : "+v"(t));
     const bool live = row < a.rows;
+    st = next_st;
+    const Bufs now = buffers(min(row, a.rows - 1));
     const int lim = live ? a.cols : 0;
     float d[V][4];  // dr
     float s0 = 0.f, s1 = 0.f;
     // dh and xh2 of a run; zero past the row
     auto values = [&](int v, float (&dh)[4], float (&xh)[4]) __attribute__((always_inline)) {
-      const int valid = lim - 4 * (t + v * TPR);
-      q.dh[v].get(dh);
-      q.r[v].get(xh);
+      const int valid = lim - 4 * (t + v * TPR), i0 = KEEP ? v : 0;
+      if constexpr (!KEEP) {
+        __builtin_amdgcn_sched_barrier(0);  // one run's registers at a time
+        qh[0].load(now.dh, t + v * TPR);
+        qr[0].load(now.r, t + v * TPR);
+      }
+      qh[i0].get(dh);
+      qr[i0].get(xh);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xh[i] = (xh[i] - q.st.z) * q.st.w;
+      for (int i = 0; i < 4; ++i) xh[i] = (xh[i] - st.z) * st.w;
       mask4(dh, valid);
       mask4(xh, valid);
     };
     // without a norm after the sum dh, r and all that is made of them are 0
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float dh[4], xh[4];
+      float dh[4], xh[4], g2[4];
       values(v, dh, xh);
-      if constexpr (!PRE) params(v, 0);
+      vec(1, v, g2);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         sums[2][v][i] += dh[i] * xh[i];
         sums[3][v][i] += dh[i];
-        const float w = dh[i] * g2[PRE ? v : 0][i];
+        const float w = dh[i] * g2[i];
         s0 += w;
         s1 += w * xh[i];
       }
@@ -229,37 +332,46 @@ __global__ __launch_bounds__(BLK) void join_bwd_kernel(JoinBackArgs a) {
     float p0 = 0.f, p1 = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = t + v * TPR, valid = lim - 4 * c, i0 = PRE ? v : 0;
-      q.d[v].get(d[v]);  // 0 if there is none
-      if constexpr (!PRE) params(v, 0);
+      const int c = t + v * TPR, valid = lim - 4 * c;
+      float g1[4], last[4];
+      const int i0 = KEEP ? v : 0;
+      if constexpr (!KEEP) {
+        qd[0].load(now.d, c);
+        qb[0].load(now.b, c);
+        if (a.gate) qg[0].load(now.g, c);
+      }
+      qd[i0].get(d[v]);  // 0 if there is none
       {
-        float dh[4], xh[4];
-        q.dh[v].opaque();
-        q.r[v].opaque();
+        float dh[4], xh[4], g2[4];
+        qh[i0].opaque();
+        qr[i0].opaque();
         values(v, dh, xh);
+        vec(1, v, g2);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[v][i] += q.st.w * (dh[i] * g2[i0][i] - s0 - xh[i] * s1);
+        for (int i = 0; i < 4; ++i) d[v][i] += st.w * (dh[i] * g2[i] - s0 - xh[i] * s1);
       }
       mask4(d[v], valid);
       if (live) {
         float o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = a.xs * d[v][i];
-        store_run4<TX>(a.dx, a.lddx, row, a.cols, c, o);
+        store_run4<TX>(a.dx, a.lddx, row, a.cols, c, o, past);
       }
+      vec(0, v, g1);
+      vec(2, v, last);
       float xh[4], g[4];
-      q.b[v].get(xh);
+      qb[i0].get(xh);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xh[i] = (xh[i] - q.st.x) * q.st.y;
+      for (int i = 0; i < 4; ++i) xh[i] = (xh[i] - st.x) * st.y;
       mask4(xh, valid);
       if (a.gate) {
-        q.g[v].get(g);
+        qg[i0].get(g);
         mask4(g, valid);
         if (live && a.dgate) {
           float o[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = a.bs * d[v][i] * (xh[i] * g1[i0][i] + last[i0][i]);
-          store_run4<TB>(a.dgate, a.lddgate, row, a.cols, c, o);
+          for (int i = 0; i < 4; ++i) o[i] = a.bs * d[v][i] * (xh[i] * g1[i] + last[i]);
+          store_run4<TB>(a.dgate, a.lddgate, row, a.cols, c, o, past);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[v][i] *= g[i];
@@ -268,56 +380,52 @@ __global__ __launch_bounds__(BLK) void join_bwd_kernel(JoinBackArgs a) {
       for (int i = 0; i < 4; ++i) {
         sums[0][v][i] += d[v][i] * xh[i];
         sums[1][v][i] += d[v][i];
-        if (!a.gate) d[v][i] *= last[i0][i];
-        d[v][i] *= a.bs * g1[i0][i];  // p (du without a norm: gamma1 is 1 then)
+        if (!a.gate) d[v][i] *= last[i];
+        d[v][i] *= a.bs * g1[i];  // p (du without a norm: gamma1 is 1 then)
         p0 += d[v][i];
         p1 += d[v][i] * xh[i];
       }
     }
+    fetch(next);
     // without a norm of the block's output its gradient is p itself (mean 0, rstd 1)
     if (post) group_total2<TPR>(p0, p1, buf[1]);
     p0 *= post_mean;
     p1 *= post ? inv_n : 0.f;
-    if (!live) return;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
+      const int i0 = KEEP ? v : 0;
       float o[4], xh[4];
-      q.b[v].opaque();
-      q.b[v].get(xh);
+      if constexpr (!KEEP) {
+        __builtin_amdgcn_sched_barrier(0);
+        qb[0].load(now.b, t + v * TPR);
+      }
+      qb[i0].opaque();
+      qb[i0].get(xh);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        o[i] = q.st.y * (d[v][i] - p0 - (post ? (xh[i] - q.st.x) * q.st.y * p1 : 0.f));
-      store_run4<TB>(a.db, a.lddb, row, a.cols, t + v * TPR, o);
+        o[i] = st.y * (d[v][i] - p0 - (post ? (xh[i] - st.x) * st.y * p1 : 0.f));
+      if (live) store_run4<TB>(a.db, a.lddb, row, a.cols, t + v * TPR, o, past);
     }
+    fetch_b(next);
   };
   const int step = gridDim.x * RPB;
   int r0 = blockIdx.x * RPB;
-  // every thread of the block runs the same number of rounds (barriers inside)
-  if constexpr (V > 1) {  // no registers for a second row
-    Row q;
-    for (int k = 0; r0 < a.rows; r0 += step, k ^= 1) {
-      // columns and parameters anew for each row: kept over the rows they spill
-      asm volatile("" : "+v"(t));
-      fetch(q, r0 + sub);
-      handle(q, r0 + sub, red[k]);
-    }
-  } else {
-    Row q0, q1;
-    fetch(q0, r0 + sub);
-    while (true) {
-      if (r0 + step < a.rows) fetch(q1, r0 + step + sub);
-      handle(q0, r0 + sub, red[0]);
-      r0 += step;
-      if (r0 >= a.rows) break;
-      if (r0 + step < a.rows) fetch(q0, r0 + step + sub);
-      handle(q1, r0 + sub, red[1]);
-      r0 += step;
-      if (r0 >= a.rows) break;
-    }
+  fetch(r0 + sub);
+  fetch_b(r0 + sub);
+  if constexpr (AT == kInLds) {
+    stage<3, COLS, BLK>(from, a.cols, vecs);
+    __syncthreads();
   }
+  if constexpr (AT == kInRegisters) {
+#pragma unroll
+    for (int n = 0; n < 3; ++n) vector4<false>(from[n], nullptr, t, a.cols, held[n]);
+  }
+  // every thread of the block runs the same number of rounds (barriers inside)
+  for (int k = 0; r0 < a.rows; r0 += step, k ^= 1) handle(r0 + sub, r0 + step + sub, red[k]);
   if (a.part == nullptr) return;
   // partial row of the workgroup: its row groups' sums in order 0, 1, ...
   float* out = a.part + (int64_t)blockIdx.x * 4 * a.cols;
+  float* join = vecs[0];
 #pragma unroll
   for (int which = 0; which < 4; ++which) {
     if constexpr (RPB > 1) {
@@ -403,59 +511,82 @@ __global__ __launch_bounds__(1024) void join_sums_kernel(JoinBackArgs a, int blo
   }
 }
 
-// Threads per row and runs of 4 columns a thread.
-struct JoinShape {
-  int tpr, v;
-};
-JoinShape join_shape(int64_t cols) {
-  if (cols <= 256) return {64, 1};
-  if (cols <= 512) return {128, 1};
-  if (cols <= 1024) return {256, 1};
-  if (cols <= 2048) return {512, 1};
-  return {1024, cols <= 4096 ? 1 : cols <= 8192 ? 2 : 4};
-}
-constexpr int bwd_block(int tpr) { return 1024 / tpr * tpr; }
+// Threads of a row. bf16: several runs of 8 bytes a thread, so that the reductions of a row
+// cost fewer instructions a column; fp32 (a stream or block in it): one run of 16 bytes.
+// Forward, us (runs x threads, in workgroups of): 16384 x 1536 bf16 3 x 128 in 512 39.2, in 256 43,
+// in 1024 50, 6 x 64 42, 2 x 192 52, 1 x 384 45; with an fp32 stream and one norm 1 x 384 in 768 47,
+// 3 x 128 50; 8192 x 4096 bf16 2 x 512 in 1024 59, 4 x 256 63, 1 x 1024 69.
+// Backward: 16384 x 1536 bf16 2 x 192 68, 1 x 384 82, 3 x 128 185 (spills); fp32 1 x 384 112, 2 x 192
+// 138. 4093 x 4096 with an fp32 stream and gates 1 x 1024 76, 2 x 512 94.
+template <typename TX, typename TB> constexpr bool kAllBf16 = sizeof(TX) + sizeof(TB) == 4;
 
-template <typename TX, typename TB, int TPR, int V>
+constexpr int fwd_block(int tpr) { return tpr == 384 ? 768 : tpr >= 512 ? 1024 : 512; }
+constexpr int bwd_block(int tpr) { return 1024 / tpr * tpr; }  // few partial rows
+
+template <typename TX, typename TB, int TPR, int V, bool LDS>
 mao_status fwd_launch(const JoinArgs& a, hipStream_t s) {
-  const int grid = std::min(a.rows, 256 * (2048 / TPR));
-  hipLaunchKernelGGL((join_fwd_kernel<TX, TB, TPR, V>), dim3(grid), dim3(TPR), 0, s, a);
+  constexpr int BLK = fwd_block(TPR);
+  const int grid = (int)std::min<int64_t>(ceil_div(a.rows, BLK / TPR), 256 * (2048 / BLK));
+  hipLaunchKernelGGL((join_fwd_kernel<TX, TB, TPR, V, BLK, LDS>), dim3(grid), dim3(BLK), 0, s, a);
   MAO_LAUNCH_CHECK();
   return MAO_OK;
 }
 
-template <typename TX, typename TB, int TPR, int V>
+template <typename TX, typename TB>
+mao_status fwd_pick(const JoinArgs& a, hipStream_t s) {
+  if constexpr (kAllBf16<TX, TB>) {
+    if (a.cols <= 256) return fwd_launch<TX, TB, 64, 1, true>(a, s);
+    if (a.cols <= 512) return fwd_launch<TX, TB, 64, 2, true>(a, s);
+    if (a.cols <= 1024) return fwd_launch<TX, TB, 128, 2, true>(a, s);
+    if (a.cols <= 1536) return fwd_launch<TX, TB, 128, 3, true>(a, s);
+    if (a.cols <= 2048) return fwd_launch<TX, TB, 256, 2, true>(a, s);
+    if (a.cols <= 4096) return fwd_launch<TX, TB, 512, 2, true>(a, s);
+  } else {
+    if (a.cols <= 256) return fwd_launch<TX, TB, 64, 1, true>(a, s);
+    if (a.cols <= 512) return fwd_launch<TX, TB, 128, 1, true>(a, s);
+    if (a.cols <= 1024) return fwd_launch<TX, TB, 256, 1, true>(a, s);
+    if (a.cols <= 1536) return fwd_launch<TX, TB, 384, 1, true>(a, s);
+    if (a.cols <= 2048) return fwd_launch<TX, TB, 512, 1, true>(a, s);
+    if (a.cols <= 4096) return fwd_launch<TX, TB, 1024, 1, true>(a, s);
+  }
+  if (a.cols <= 8192) return fwd_launch<TX, TB, 1024, 2, false>(a, s);
+  return fwd_launch<TX, TB, 1024, 4, false>(a, s);
+}
+
+int bwd_threads(bool all_bf16, int64_t cols) {
+  if (cols <= 256) return 64;
+  if (cols > 4096) return 1024;
+  const int t = cols <= 512 ? 64 : cols <= 1024 ? 128 : cols <= 1536 ? 192 : cols <= 2048 ? 256 : 512;
+  return all_bf16 ? t : 2 * t;
+}
+
+template <typename TX, typename TB, int TPR, int V, bool LDS>
 mao_status bwd_launch(const JoinBackArgs& a, hipStream_t s) {
   constexpr int BLK = bwd_block(TPR);
-  hipLaunchKernelGGL((join_bwd_kernel<TX, TB, TPR, V, BLK>), dim3(join_blocks(a.rows, a.cols)),
-                     dim3(BLK), 0, s, a);
+  const int grid = join_blocks(kAllBf16<TX, TB>, a.rows, a.cols);
+  hipLaunchKernelGGL((join_bwd_kernel<TX, TB, TPR, V, BLK, LDS>), dim3(grid), dim3(BLK), 0, s, a);
   MAO_LAUNCH_CHECK();
   return MAO_OK;
 }
 
-#define MAO_JOIN_PICK(NAME, GO, ARGS)                  \
-  template <typename TX, typename TB>                  \
-  mao_status NAME(const ARGS& a, hipStream_t s) {      \
-    const JoinShape k = join_shape(a.cols);            \
-    switch (k.tpr) {                                   \
-      case 64: return GO<TX, TB, 64, 1>(a, s);         \
-      case 128: return GO<TX, TB, 128, 1>(a, s);       \
-      case 256: return GO<TX, TB, 256, 1>(a, s);       \
-      case 512: return GO<TX, TB, 512, 1>(a, s);       \
-      default: break;                                  \
-    }                                                  \
-    if (k.v == 1) return GO<TX, TB, 1024, 1>(a, s);    \
-    if (k.v == 2) return GO<TX, TB, 1024, 2>(a, s);    \
-    return GO<TX, TB, 1024, 4>(a, s);                  \
-  }
-MAO_JOIN_PICK(fwd_pick, fwd_launch, JoinArgs)
-MAO_JOIN_PICK(bwd_pick, bwd_launch, JoinBackArgs)
-#undef MAO_JOIN_PICK
+template <typename TX, typename TB>
+mao_status bwd_pick(const JoinBackArgs& a, hipStream_t s) {
+  constexpr bool H = kAllBf16<TX, TB>;
+  constexpr int V = H ? 2 : 1, M = H ? 1 : 2;
+  if (a.cols <= 256) return bwd_launch<TX, TB, 64, 1, true>(a, s);
+  if (a.cols <= 512) return bwd_launch<TX, TB, 64 * M, V, true>(a, s);
+  if (a.cols <= 1024) return bwd_launch<TX, TB, 128 * M, V, true>(a, s);
+  if (a.cols <= 1536) return bwd_launch<TX, TB, 192 * M, V, true>(a, s);
+  if (a.cols <= 2048) return bwd_launch<TX, TB, 256 * M, V, true>(a, s);
+  if (a.cols <= 4096) return bwd_launch<TX, TB, 512 * M, V, true>(a, s);
+  if (a.cols <= 8192) return bwd_launch<TX, TB, 1024, 2, true>(a, s);
+  return bwd_launch<TX, TB, 1024, 4, false>(a, s);
+}
 
 }  // namespace
 
-int join_blocks(int64_t rows, int64_t cols) {
-  const int tpr = join_shape(cols).tpr;
+int join_blocks(bool all_bf16, int64_t rows, int64_t cols) {
+  const int tpr = bwd_threads(all_bf16, cols);
   return (int)std::min<int64_t>(ceil_div(rows, bwd_block(tpr) / tpr), 256);
 }
 
@@ -473,7 +604,7 @@ mao_status launch_join_backward(const JoinBackArgs& a, int stream_type, int bloc
     MAO_TRY((block_type == MAO_BF16 ? bwd_pick<float, bf16_t>(a, s) : bwd_pick<float, float>(a, s)));
   if (a.part == nullptr) return MAO_OK;
   hipLaunchKernelGGL(join_sums_kernel, dim3((int)ceil_div(a.cols, 64), 2), dim3(1024), 0, s, a,
-                     join_blocks(a.rows, a.cols));
+                     join_blocks(stream_type == MAO_BF16 && block_type == MAO_BF16, a.rows, a.cols));
   MAO_LAUNCH_CHECK();
   return MAO_OK;
 }

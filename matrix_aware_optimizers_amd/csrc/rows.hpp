@@ -73,6 +73,13 @@ __device__ __forceinline__ void group_total2(float& a, float& b, float2* buf) {
       const float2 t0 = buf[w0], t1 = buf[w0 + 1], t2 = buf[w0 + 2];
       a = (t0.x + t1.x) + t2.x;
       b = (t0.y + t1.y) + t2.y;
+    } else if constexpr ((NW & (NW - 1)) != 0) {
+      a = b = 0.f;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        a += buf[w0 + i].x;
+        b += buf[w0 + i].y;
+      }
     } else {  // one partial sum per lane, joined across 2, 4, 8 or 16 lanes
       const float2 t = buf[w0 + (threadIdx.x & (NW - 1))];
       a = dpp_add<0xB1>(t.x);
@@ -153,18 +160,25 @@ template <typename T> __device__ __forceinline__ int run4_bytes(int cols) {
   return (cols + 3) / 4 * 4 * (int)sizeof(T);
 }
 
-// Writes run `run` of a row.
+// Writes run `run` of a row; past: past the L2.
 template <typename T>
 __device__ __forceinline__ void store_run4(void* p, int64_t ld, int row, int cols, int run,
-                                           const float (&v)[4]) {
+                                           const float (&v)[4], bool past) {
+  constexpr int NT = 2;
   const auto whole = row_buffer(p, ld * (int64_t)sizeof(T), row, cols / 4 * 4 * (int)sizeof(T));
   if constexpr (sizeof(T) == 2) {
     const u32x2 k = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-    __builtin_amdgcn_raw_buffer_store_b64(k, whole, run * 8, 0, 0);
+    if (past)
+      __builtin_amdgcn_raw_buffer_store_b64(k, whole, run * 8, 0, NT);
+    else
+      __builtin_amdgcn_raw_buffer_store_b64(k, whole, run * 8, 0, 0);
   } else {
     const u32x4 k = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
                      __float_as_uint(v[3])};
-    __builtin_amdgcn_raw_buffer_store_b128(k, whole, run * 16, 0, 0);
+    if (past)
+      __builtin_amdgcn_raw_buffer_store_b128(k, whole, run * 16, 0, NT);
+    else
+      __builtin_amdgcn_raw_buffer_store_b128(k, whole, run * 16, 0, 0);
   }
   const int n = cols - 4 * run;
   if (n > 0 && n < 4) {
