@@ -238,9 +238,21 @@ __global__ __launch_bounds__(BLK) void join_bwd_kernel(JoinBackArgs a) {
       vector4<AT == kInLds>(from[n], vecs[AT == kInLds ? n : 0], t + v * TPR, a.cols, w);
     }
   };
-  float sums[4][V][4];  // A, D, dgamma2, dbeta2
+  // A, D, dgamma2, dbeta2. With four runs a thread the last two are in LDS, each thread's its
+  // own (2048 x 16384 bf16 180 us; in registers, which spilt, 341).
+  constexpr bool HALF = V > 2;
+  constexpr int S = HALF ? 2 : 4;
+  __shared__ float rest[HALF ? 2 : 1][HALF ? COLS : 1];
+  float sums[S][V][4];
+  if constexpr (HALF) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        *(float4*)&rest[k][4 * (t + v * TPR)] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll
+  for (int k = 0; k < S; ++k)
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -317,10 +329,29 @@ __global__ __launch_bounds__(BLK) void join_bwd_kernel(JoinBackArgs a) {
       float dh[4], xh[4], g2[4];
       values(v, dh, xh);
       vec(1, v, g2);
+      if constexpr (HALF) {
+        float4* p0 = (float4*)&rest[0][4 * (t + v * TPR)];
+        float4* p1 = (float4*)&rest[HALF ? 1 : 0][4 * (t + v * TPR)];
+        float4 k0 = *p0, k1 = *p1;
+        k0.x += dh[0] * xh[0];
+        k0.y += dh[1] * xh[1];
+        k0.z += dh[2] * xh[2];
+        k0.w += dh[3] * xh[3];
+        k1.x += dh[0];
+        k1.y += dh[1];
+        k1.z += dh[2];
+        k1.w += dh[3];
+        *p0 = k0;
+        *p1 = k1;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sums[S - 2][v][i] += dh[i] * xh[i];
+          sums[S - 1][v][i] += dh[i];
+        }
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        sums[2][v][i] += dh[i] * xh[i];
-        sums[3][v][i] += dh[i];
         const float w = dh[i] * g2[i];
         s0 += w;
         s1 += w * xh[i];
@@ -437,7 +468,7 @@ __global__ __launch_bounds__(BLK) void join_bwd_kernel(JoinBackArgs a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               float* p = &join[(v * 4 + i) * TPR + t];
-              *p = k == 0 ? sums[which][v][i] : *p + sums[which][v][i];
+              *p = k == 0 ? sums[which < S ? which : 0][v][i] : *p + sums[which < S ? which : 0][v][i];
             }
         }
       }
@@ -449,7 +480,11 @@ __global__ __launch_bounds__(BLK) void join_bwd_kernel(JoinBackArgs a) {
         const int c = t + v * TPR;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float w = sums[which][v][i] + (RPB > 1 ? join[RPB > 1 ? (v * 4 + i) * TPR + t : 0] : 0.f);
+          float w = RPB > 1 ? join[RPB > 1 ? (v * 4 + i) * TPR + t : 0] : 0.f;
+          if (HALF && which >= 2)
+            w += rest[HALF ? which - 2 : 0][HALF ? 4 * c + i : 0];
+          else
+            w += sums[which < S ? which : 0][v][i];
           if (4 * c + i < a.cols) out[(int64_t)which * a.cols + 4 * c + i] = w;
         }
       }
