@@ -69,6 +69,26 @@ def test_step_aliases():
 
 
 @needs_no_gpu
+@pytest.mark.parametrize("count", [2, 3, 16, 64, 65, 66, 300])
+@pytest.mark.parametrize("runs", [1, 2, 5, 31, 32, 33, 1000])
+def test_step_alias_orders(count, runs):
+    """One pair that overlaps is found, and no other, in whatever order the buffers lie."""
+    rng = np.random.default_rng(count * 1000 + runs)
+    order = np.arange(count)
+    for part in np.array_split(order, min(runs, count)):
+        rng.shuffle(part)  # in place, a view
+    places = [item(int(k)) for k in order]
+    rest = [p for p in places]
+    assert step(rest) != E_ALIAS  # fails at the launch, for want of a device
+    for name, of in (("w", "m"), ("g", "v"), ("v", "g")):
+        i, j = int(rng.integers(count)), int(rng.integers(count - 1))
+        j += j >= i
+        bad = [p for p in places]
+        bad[i] = item(int(order[i]), **{name: getattr(places[j], of) + 3996})
+        assert step(bad) == E_ALIAS, (name, i, j)
+
+
+@needs_no_gpu
 def test_read_refusals():
     def read(n=1000, dtype=0, count=1, null=False, **at):
         a = {k: FAKE + j * MB for j, k in enumerate(("m", "v", "ms", "vs", "mo", "vo"))}
