@@ -82,8 +82,7 @@ class MlpBlock:
         for k, w in self.matrices.items():
             mao.foam_step(w, grads[k], self.foam[k], t, lr=lr, fwd_rot="bf16x3",
                           refresh_prod="bf16x3", back_rot_dtype="bf16")
-        for k, v in self.vectors.items():
-            mao.adamw_step(v, grads[k], *self.adam[k], t, lr=lr)
+        mao.adamw_step_many([(v, grads[k], *self.adam[k]) for k, v in self.vectors.items()], t, lr=lr)
 
 
 def train(width, hidden, tokens, steps, keep, lr=2e-3, seed=0, device="cuda"):

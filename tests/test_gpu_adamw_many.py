@@ -235,6 +235,33 @@ def test_8bit_zero_and_tiny_values(gpu_lib):
     assert (m[768:] == 0).all()
 
 
+def test_8bit_many(gpu_lib):
+    """More tensors and rates than one launch holds, of both kinds of state: what single calls
+    give, read back in one call too."""
+    import torch
+    log("many 8-bit")
+    items = []
+    for i in range(150):
+        w = _rand(5 * i, SIZES[i % 11] + i // 11, ("f32", "bf16")[i % 2])
+        g = _rand(5 * i + 1, w.numel(), ("f32", "bf16")[i // 2 % 2])
+        items.append((w, g, *gpu_lib.adamw8_state(w)) if i % 5 else
+                     (w, g, _rand(5 * i + 2, w.numel()), _rand(5 * i + 3, w.numel()).square()))
+    want = [tuple(t.clone() for t in it) for it in items]
+    lr = [1e-3 * (1 + i % 23) for i in range(len(items))]
+    for t in (1, 2):
+        gpu_lib.adamw_step_many(items, t, lr=lr, weight_decay=0.1)
+        for it, a in zip(want, lr):
+            gpu_lib.adamw_step_many([it], t, lr=a, weight_decay=0.1)
+    torch.cuda.synchronize()
+    for x, y in zip(items, want):
+        for p, q in zip(x, y):
+            assert torch.equal(p, q)
+    states = [it[2:] for it in items if len(it) == 6]
+    for got, st in zip(gpu_lib.adamw8_read(states), states):
+        one, = gpu_lib.adamw8_read([st])
+        assert torch.equal(got[0], one[0]) and torch.equal(got[1], one[1])
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_8bit_not_finite(gpu_lib, bad):
     """A span with a NaN or an infinity reads as NaN, all of it; the others do not."""
@@ -360,13 +387,13 @@ def test_refusals(gpu_lib):
 
 
 def test_far_offsets(gpu_lib):
-    """More than 2^31 elements: the last ones are stepped as a short tensor of the same
+    """More than 2^32 elements: the last ones are stepped as a short tensor of the same
     values with the same place in their span."""
     import torch
     if torch.cuda.mem_get_info()[0] < 40 << 30:
         pytest.skip("40 GiB of free GPU memory are needed")
     log("far offsets")
-    n = (1 << 31) + 256 * 3 + 5
+    n = (1 << 32) + 256 * 3 + 5
     tail = 256 * 2 + 5
     w = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
     g = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
