@@ -1,9 +1,10 @@
 """Matrix-aware optimizer steps (Muon, Muon+, SOAP, FOAM, AdamW) on AMD MI355X,
 and the layer operators that make their gradients (layer norm, linear layer,
-8-bit activation checkpoints).
+8-bit activation checkpoints, joins with the residual stream, log probabilities of
+tokens and the loss).
 
 Thin binding over ``libmao.so`` (declared in ``include/mao.h``): ctypes for the
-steps, the C++ extension ``_layers.so`` for the layer operators. The binding only
+steps, the C++ extension ``_layers.so`` for the layer operators and lists of tensors. The binding only
 marshals arguments: every step runs in the library's HIP
 kernels, on the current torch stream. PyTorch provides device memory and
 streams; the library itself allocates nothing, so the workspace is a torch
