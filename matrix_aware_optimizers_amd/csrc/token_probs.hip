@@ -383,7 +383,7 @@ __global__ __launch_bounds__(THREADS) void token_kernel(TokenArgs a) {
     for (int r = 0; r < R; ++r) {
       const int run = base + r * THREADS;
       // past the end: the row's first run once more, replaced below
-      raw[r].load_cut(x + 8 * (int64_t)(run < runs ? run : 0), run < runs ? a.vocab - 8 * run : 8);
+      raw[r].load_cut(x + 8 * (int64_t)(run < runs ? run : 0), a.vocab - (run < runs ? 8 * run : 0));
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -590,7 +590,8 @@ __global__ __launch_bounds__(THREADS) void token_loss_kernel(TokenBackArgs a) {
   float w = a.weight && live ? a.weight[row] : 1.f;
   if (target >= a.vocab) w = NAN;
   if (q.s == 0.f) w = 0.f;  // no finite logit
-  const float scale = q.s == 0.f ? 0.f : w / q.s;
+  const float scale = w / q.s;
+  const bool nothing = !live || w == 0.f;
   if (a.logprob && hit < 0 && tid == 0) a.logprob[row] = live ? NAN : 0.f;
   auto finish = [&](Piece<T>& k, int piece) __attribute__((always_inline)) {
     float v[W];
@@ -604,7 +605,7 @@ __global__ __launch_bounds__(THREADS) void token_loss_kernel(TokenBackArgs a) {
       for (int i = 0; i < W; ++i) xt = i == at ? v[i] : xt;
     }
 #pragma unroll
-    for (int i = 0; i < W; ++i) v[i] = live ? exp_hw(v[i] - q.m) * scale : 0.f;
+    for (int i = 0; i < W; ++i) v[i] = nothing ? 0.f : exp_hw(v[i] - q.m) * scale;
     if (here) {
       if (a.logprob) a.logprob[row] = log_prob(xt, q, q.s == 0.f ? 0.f : logf(q.s));
 #pragma unroll

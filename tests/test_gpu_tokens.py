@@ -313,6 +313,25 @@ def test_rows_without_a_target_may_hold_anything(gpu_lib):
     assert (lp[[1, 3, 4]] == 0).all() and (f.logprob[[1, 3, 4]] == 0).all()
 
 
+@pytest.mark.parametrize("vocab", [5, 3000, 200003])
+def test_rows_of_weight_zero_may_hold_anything(gpu_lib, vocab):
+    """As for the backward call: no gradient, while the log probabilities are the rows' own."""
+    import torch
+    log(f"rows of weight zero {vocab}")
+    x, _ = _logits(4, 5, vocab)
+    X = _dev(x, "bf16")
+    X[1], X[3] = float("nan"), float("inf")
+    t, w = _targets([1, 2, 3, 4, 0]), torch.tensor([1.0, 0.0, 0.0, -0.0, 2.0], device="cuda")
+    want = gpu_lib.token_logprobs(X, t)
+    one = gpu_lib.token_loss(X[4:], t[4:], w[4:])
+    lp, dx = gpu_lib.token_loss(X, t, w)
+    assert torch.isfinite(dx).all() and (dx[1:4] == 0).all() and dx[[0, 4]].any(dim=1).all()
+    assert torch.equal(dx[4:], one[1])
+    assert torch.isnan(lp[[1, 3]]).all() and torch.isnan(want.logprob[[1, 3]]).all()
+    # each within 170 + 2 |lp| + 6 log S (both below 20) steps of 2^-24 of the formula's
+    assert (lp[[0, 2, 4]] - want.logprob[[0, 2, 4]]).abs().max() < 2 * 330 * R
+
+
 def test_captured(gpu_lib):
     """Two graphs of calls and a larger eager call between their
     replays: every replay equals the eager results, new logits included."""
