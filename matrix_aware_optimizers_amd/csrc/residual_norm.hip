@@ -42,9 +42,9 @@ __device__ __forceinline__ bool past_l2(int rows, int cols) {
   return (int64_t)rows * cols >= (int64_t)1 << 23;
 }
 
-// Parameter vectors of a workgroup in LDS, as fp32 (LDS: up to 4096 columns forward, 8192
+// Parameter vectors of a workgroup in LDS, as fp32 (LDS: up to 6144 columns forward, 8192
 // backward; rows of a CU read them from there instead of holding 5 values a column in
-// registers), or read where they are.
+// registers), in registers, or read where they are.
 struct Vector {
   const void* p;  // or nullptr: dflt
   int dtype;
@@ -74,9 +74,13 @@ __device__ __forceinline__ void stage(const Vector (&from)[N], int cols, float (
       if (c < COLS) to[n][c] = from[n].p ? __uint_as_float(u) : from[n].dflt;
     }
 }
-// Where a kernel has its vectors: a thread with one run of columns keeps their values.
+// Where a kernel has its vectors: a thread with one run of columns keeps their values, and one with
+// two where LDS has no room for them (forward 4096 x 8192 bf16 80 us, read for each row 90;
+// 6106 x 8187 from fp32 113 for 157).
 enum { kInRegisters, kInLds, kInMemory };
-constexpr int vectors_at(int v, bool lds) { return v == 1 ? kInRegisters : lds ? kInLds : kInMemory; }
+constexpr int vectors_at(int v, bool lds) {
+  return v == 1 ? kInRegisters : lds ? kInLds : v == 2 ? kInRegisters : kInMemory;
+}
 
 template <bool LDS>
 __device__ __forceinline__ void vector4(const Vector& from, const float* staged, int run, int cols,
@@ -107,11 +111,11 @@ __global__ __launch_bounds__(BLK) void join_fwd_kernel(JoinArgs a) {
                           {a.gate_vec, a.gate_dtype, 1.f}, {a.pre.gamma, a.pre.p_dtype, 1.f},
                           {a.pre.beta, a.pre.p_dtype, 0.f}};
   constexpr int AT = vectors_at(V, LDS);
-  float held[AT == kInRegisters ? 5 : 1][4];
+  float held[AT == kInRegisters ? 5 : 1][AT == kInRegisters ? V : 1][4];
   auto vec = [&](int n, int v, float (&w)[4]) __attribute__((always_inline)) {
     if constexpr (AT == kInRegisters) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = held[AT == kInRegisters ? n : 0][i];
+      for (int i = 0; i < 4; ++i) w[i] = held[AT == kInRegisters ? n : 0][AT == kInRegisters ? v : 0][i];
     } else {
       vector4<AT == kInLds>(from[n], vecs[AT == kInLds ? n : 0], t + v * TPR, a.cols, w);
     }
@@ -140,7 +144,9 @@ __global__ __launch_bounds__(BLK) void join_fwd_kernel(JoinArgs a) {
   }
   if constexpr (AT == kInRegisters) {
 #pragma unroll
-    for (int n = 0; n < 5; ++n) vector4<false>(from[n], nullptr, t, a.cols, held[n]);
+    for (int n = 0; n < 5; ++n)
+#pragma unroll
+      for (int v = 0; v < V; ++v) vector4<false>(from[n], nullptr, t + v * TPR, a.cols, held[n][v]);
   }
   // every thread of the block runs the same number of rounds (barriers inside)
   for (; r0 < a.rows; r0 += step, turn ^= 1) {
@@ -236,11 +242,11 @@ __global__ __launch_bounds__(BLK) void join_bwd_kernel(JoinBackArgs a) {
   const Vector from[3] = {{a.post.gamma, a.post.p_dtype, 1.f}, {a.pre.gamma, a.pre.p_dtype, 1.f},
                           {a.gate ? a.post.beta : a.gate_vec, a.gate ? a.post.p_dtype : a.gate_dtype,
                            a.gate ? 0.f : 1.f}};
-  float held[AT == kInRegisters ? 3 : 1][4];
+  float held[AT == kInRegisters ? 3 : 1][AT == kInRegisters ? V : 1][4];
   auto vec = [&](int n, int v, float (&w)[4]) __attribute__((always_inline)) {
     if constexpr (AT == kInRegisters) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = held[AT == kInRegisters ? n : 0][i];
+      for (int i = 0; i < 4; ++i) w[i] = held[AT == kInRegisters ? n : 0][AT == kInRegisters ? v : 0][i];
     } else {
       vector4<AT == kInLds>(from[n], vecs[AT == kInLds ? n : 0], t + v * TPR, a.cols, w);
     }
@@ -456,7 +462,9 @@ __global__ __launch_bounds__(BLK) void join_bwd_kernel(JoinBackArgs a) {
   }
   if constexpr (AT == kInRegisters) {
 #pragma unroll
-    for (int n = 0; n < 3; ++n) vector4<false>(from[n], nullptr, t, a.cols, held[n]);
+    for (int n = 0; n < 3; ++n)
+#pragma unroll
+      for (int v = 0; v < V; ++v) vector4<false>(from[n], nullptr, t + v * TPR, a.cols, held[n][v]);
   }
   // every thread of the block runs the same number of rounds (barriers inside)
   for (int k = 0; r0 < a.rows; r0 += step, k ^= 1) handle(r0 + sub, r0 + step + sub, red[k]);
@@ -557,12 +565,14 @@ __global__ __launch_bounds__(1024) void join_sums_kernel(JoinBackArgs a, int blo
 // cost fewer instructions a column; fp32 (a stream or block in it): one run of 16 bytes.
 // Forward, us (runs x threads, in workgroups of): 16384 x 1536 bf16 3 x 128 in 512 39.2, in 256 43,
 // in 1024 50, 6 x 64 42, 2 x 192 52, 1 x 384 45; with an fp32 stream and one norm 1 x 384 in 768 47,
-// 3 x 128 50; 8192 x 4096 bf16 2 x 512 in 1024 59, 4 x 256 63, 1 x 1024 69.
+// 3 x 128 50; 8192 x 4096 bf16 2 x 512 in 1024 59, 4 x 256 63, 1 x 1024 69; 8192 x 6144 bf16 3 x 512
+// in 1024 102, 2 x 768 122, 2 x 1024 143; 4096 x 5120 fp32 2 x 768 80, 2 x 1024 82.
 // Backward: 16384 x 1536 bf16 2 x 192 68, 1 x 384 82, 3 x 128 185 (spills); fp32 1 x 384 112, 2 x 192
-// 138. 4093 x 4096 with an fp32 stream and gates 1 x 1024 76, 2 x 512 94.
+// 138. 4093 x 4096 with an fp32 stream and gates 1 x 1024 76, 2 x 512 94. 8192 x 6144 bf16 2 x 768
+// 139, 2 x 1024 155; 4096 x 5120 fp32 104 and 130.
 template <typename TX, typename TB> constexpr bool kAllBf16 = sizeof(TX) + sizeof(TB) == 4;
 
-constexpr int fwd_block(int tpr) { return tpr == 384 ? 768 : tpr >= 512 ? 1024 : 512; }
+constexpr int fwd_block(int tpr) { return tpr % 384 == 0 ? 768 : tpr >= 512 ? 1024 : 512; }
 constexpr int bwd_block(int tpr) { return 1024 / tpr * tpr; }  // few partial rows
 
 template <typename TX, typename TB, int TPR, int V, bool LDS>
@@ -583,6 +593,7 @@ mao_status fwd_pick(const JoinArgs& a, hipStream_t s) {
     if (a.cols <= 1536) return fwd_launch<TX, TB, 128, 3, true>(a, s);
     if (a.cols <= 2048) return fwd_launch<TX, TB, 256, 2, true>(a, s);
     if (a.cols <= 4096) return fwd_launch<TX, TB, 512, 2, true>(a, s);
+    if (a.cols <= 6144) return fwd_launch<TX, TB, 512, 3, true>(a, s);
   } else {
     if (a.cols <= 256) return fwd_launch<TX, TB, 64, 1, true>(a, s);
     if (a.cols <= 512) return fwd_launch<TX, TB, 128, 1, true>(a, s);
@@ -590,6 +601,7 @@ mao_status fwd_pick(const JoinArgs& a, hipStream_t s) {
     if (a.cols <= 1536) return fwd_launch<TX, TB, 384, 1, true>(a, s);
     if (a.cols <= 2048) return fwd_launch<TX, TB, 512, 1, true>(a, s);
     if (a.cols <= 4096) return fwd_launch<TX, TB, 1024, 1, true>(a, s);
+    if (a.cols <= 6144) return fwd_launch<TX, TB, 768, 2, false>(a, s);
   }
   if (a.cols <= 8192) return fwd_launch<TX, TB, 1024, 2, false>(a, s);
   return fwd_launch<TX, TB, 1024, 4, false>(a, s);
@@ -597,7 +609,7 @@ mao_status fwd_pick(const JoinArgs& a, hipStream_t s) {
 
 int bwd_threads(bool all_bf16, int64_t cols) {
   if (cols <= 256) return 64;
-  if (cols > 4096) return 1024;
+  if (cols > 4096) return cols <= 6144 ? 768 : 1024;
   const int t = cols <= 512 ? 64 : cols <= 1024 ? 128 : cols <= 1536 ? 192 : cols <= 2048 ? 256 : 512;
   return all_bf16 ? t : 2 * t;
 }
@@ -621,6 +633,7 @@ mao_status bwd_pick(const JoinBackArgs& a, hipStream_t s) {
   if (a.cols <= 1536) return bwd_launch<TX, TB, 192 * M, V, true>(a, s);
   if (a.cols <= 2048) return bwd_launch<TX, TB, 256 * M, V, true>(a, s);
   if (a.cols <= 4096) return bwd_launch<TX, TB, 512 * M, V, true>(a, s);
+  if (a.cols <= 6144) return bwd_launch<TX, TB, 768, 2, true>(a, s);
   if (a.cols <= 8192) return bwd_launch<TX, TB, 1024, 2, true>(a, s);
   return bwd_launch<TX, TB, 1024, 4, false>(a, s);
 }

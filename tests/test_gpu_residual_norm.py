@@ -216,8 +216,8 @@ def test_kinds(gpu_lib, post, pre, gate):
         _run(gpu_lib, Case(9 + k, 5, 1540, xt, bt, post, pre, gate), dr=pre == "none")
 
 
-COLS = [1, 2, 3, 4, 5, 8, 64, 255, 256, 257, 511, 513, 1000, 1025, 1536, 2048, 2049, 4096, 4100, 8192,
-        8193, 16384]
+COLS = [1, 2, 3, 4, 5, 8, 64, 255, 256, 257, 511, 513, 1000, 1025, 1536, 2048, 2049, 4096, 4100, 5120,
+        6144, 6145, 8192, 8193, 16384]
 
 
 @pytest.mark.parametrize("cols", COLS)
@@ -247,6 +247,14 @@ def test_parameters_left_out(gpu_lib):
     b = gpu_lib.residual_norm_backward(c.dH, c.dR, c.B, r, st, post="layer", sums=False)
     assert torch.equal(a.dX, b.dX) and torch.equal(a.dB, b.dB)
     assert b[2:] == (None,) * 5 and a.dpost_gamma is not None and a.dpre_beta is None
+
+
+@pytest.mark.parametrize("rows,cols", [(1100, 5121), (600, 7003), (600, 9001)])
+@pytest.mark.parametrize("types", [("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32")])
+def test_wide_rows_in_turn(gpu_lib, rows, cols, types):
+    """More rows than workgroups at once, each with several runs a thread."""
+    log(f"wide rows {rows} x {cols} {types}")
+    _run(gpu_lib, Case(3, rows, cols, *types, "layer", "rms", "vector"))
 
 
 @pytest.mark.parametrize("cols", [30, 1030, 8200])
