@@ -566,13 +566,17 @@ __global__ __launch_bounds__(1024) void join_sums_kernel(JoinBackArgs a, int blo
 // Forward, us (runs x threads, in workgroups of): 16384 x 1536 bf16 3 x 128 in 512 39.2, in 256 43,
 // in 1024 50, 6 x 64 42, 2 x 192 52, 1 x 384 45; with an fp32 stream and one norm 1 x 384 in 768 47,
 // 3 x 128 50; 8192 x 4096 bf16 2 x 512 in 1024 59, 4 x 256 63, 1 x 1024 69; 8192 x 6144 bf16 3 x 512
-// in 1024 102, 2 x 768 122, 2 x 1024 143; 4096 x 5120 fp32 2 x 768 80, 2 x 1024 82.
+// in 1024 102, 2 x 768 122, 2 x 1024 143; 4096 x 5120 fp32 2 x 768 80, 2 x 1024 82; 8192 x 2560 bf16
+// 2 x 320 in 640 43, in 960 44, 2 x 512 59; 16384 x 768 bf16 3 x 64 21, 1 x 192 25, 2 x 128 26.
 // Backward: 16384 x 1536 bf16 2 x 192 68, 1 x 384 82, 3 x 128 185 (spills); fp32 1 x 384 112, 2 x 192
 // 138. 4093 x 4096 with an fp32 stream and gates 1 x 1024 76, 2 x 512 94. 8192 x 6144 bf16 2 x 768
-// 139, 2 x 1024 155; 4096 x 5120 fp32 104 and 130.
+// 139, 2 x 1024 155; 4096 x 5120 fp32 104 and 130; 8192 x 2560 bf16 2 x 320 61, 2 x 512 76, fp32
+// 1 x 640 99, 1 x 1024 103; 16384 x 768 bf16 1 x 192 36, 2 x 128 43, fp32 1 x 192 62, 1 x 256 61.
 template <typename TX, typename TB> constexpr bool kAllBf16 = sizeof(TX) + sizeof(TB) == 4;
 
-constexpr int fwd_block(int tpr) { return tpr % 384 == 0 ? 768 : tpr >= 512 ? 1024 : 512; }
+constexpr int fwd_block(int tpr) {
+  return tpr % 192 == 0 ? 768 : tpr == 320 ? 640 : tpr >= 512 ? 1024 : 512;
+}
 constexpr int bwd_block(int tpr) { return 1024 / tpr * tpr; }  // few partial rows
 
 template <typename TX, typename TB, int TPR, int V, bool LDS>
@@ -589,14 +593,17 @@ mao_status fwd_pick(const JoinArgs& a, hipStream_t s) {
   if constexpr (kAllBf16<TX, TB>) {
     if (a.cols <= 256) return fwd_launch<TX, TB, 64, 1, true>(a, s);
     if (a.cols <= 512) return fwd_launch<TX, TB, 64, 2, true>(a, s);
+    if (a.cols <= 768) return fwd_launch<TX, TB, 64, 3, true>(a, s);
     if (a.cols <= 1024) return fwd_launch<TX, TB, 128, 2, true>(a, s);
     if (a.cols <= 1536) return fwd_launch<TX, TB, 128, 3, true>(a, s);
     if (a.cols <= 2048) return fwd_launch<TX, TB, 256, 2, true>(a, s);
+    if (a.cols <= 2560) return fwd_launch<TX, TB, 320, 2, true>(a, s);
     if (a.cols <= 4096) return fwd_launch<TX, TB, 512, 2, true>(a, s);
     if (a.cols <= 6144) return fwd_launch<TX, TB, 512, 3, true>(a, s);
   } else {
     if (a.cols <= 256) return fwd_launch<TX, TB, 64, 1, true>(a, s);
     if (a.cols <= 512) return fwd_launch<TX, TB, 128, 1, true>(a, s);
+    if (a.cols <= 768) return fwd_launch<TX, TB, 192, 1, true>(a, s);
     if (a.cols <= 1024) return fwd_launch<TX, TB, 256, 1, true>(a, s);
     if (a.cols <= 1536) return fwd_launch<TX, TB, 384, 1, true>(a, s);
     if (a.cols <= 2048) return fwd_launch<TX, TB, 512, 1, true>(a, s);
@@ -609,8 +616,14 @@ mao_status fwd_pick(const JoinArgs& a, hipStream_t s) {
 
 int bwd_threads(bool all_bf16, int64_t cols) {
   if (cols <= 256) return 64;
+  if (cols > 512 && cols <= 768) return 192;
   if (cols > 4096) return cols <= 6144 ? 768 : 1024;
-  const int t = cols <= 512 ? 64 : cols <= 1024 ? 128 : cols <= 1536 ? 192 : cols <= 2048 ? 256 : 512;
+  const int t = cols <= 512    ? 64
+                : cols <= 1024 ? 128
+                : cols <= 1536 ? 192
+                : cols <= 2048 ? 256
+                : cols <= 2560 ? 320
+                               : 512;
   return all_bf16 ? t : 2 * t;
 }
 
@@ -629,9 +642,11 @@ mao_status bwd_pick(const JoinBackArgs& a, hipStream_t s) {
   constexpr int V = H ? 2 : 1, M = H ? 1 : 2;
   if (a.cols <= 256) return bwd_launch<TX, TB, 64, 1, true>(a, s);
   if (a.cols <= 512) return bwd_launch<TX, TB, 64 * M, V, true>(a, s);
+  if (a.cols <= 768) return bwd_launch<TX, TB, 192, 1, true>(a, s);
   if (a.cols <= 1024) return bwd_launch<TX, TB, 128 * M, V, true>(a, s);
   if (a.cols <= 1536) return bwd_launch<TX, TB, 192 * M, V, true>(a, s);
   if (a.cols <= 2048) return bwd_launch<TX, TB, 256 * M, V, true>(a, s);
+  if (a.cols <= 2560) return bwd_launch<TX, TB, 320 * M, V, true>(a, s);
   if (a.cols <= 4096) return bwd_launch<TX, TB, 512 * M, V, true>(a, s);
   if (a.cols <= 6144) return bwd_launch<TX, TB, 768, 2, true>(a, s);
   if (a.cols <= 8192) return bwd_launch<TX, TB, 1024, 2, true>(a, s);

@@ -216,8 +216,8 @@ def test_kinds(gpu_lib, post, pre, gate):
         _run(gpu_lib, Case(9 + k, 5, 1540, xt, bt, post, pre, gate), dr=pre == "none")
 
 
-COLS = [1, 2, 3, 4, 5, 8, 64, 255, 256, 257, 511, 513, 1000, 1025, 1536, 2048, 2049, 4096, 4100, 5120,
-        6144, 6145, 8192, 8193, 16384]
+COLS = [1, 2, 3, 4, 5, 8, 64, 255, 256, 257, 511, 513, 768, 770, 1000, 1025, 1536, 2048, 2049, 2560, 2563,
+        4096, 4100, 5120, 6144, 6145, 8192, 8193, 16384]
 
 
 @pytest.mark.parametrize("cols", COLS)
@@ -249,7 +249,7 @@ def test_parameters_left_out(gpu_lib):
     assert b[2:] == (None,) * 5 and a.dpost_gamma is not None and a.dpre_beta is None
 
 
-@pytest.mark.parametrize("rows,cols", [(1100, 5121), (600, 7003), (600, 9001)])
+@pytest.mark.parametrize("rows,cols", [(2300, 601), (1100, 2501), (1100, 5121), (600, 7003), (600, 9001)])
 @pytest.mark.parametrize("types", [("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32")])
 def test_wide_rows_in_turn(gpu_lib, rows, cols, types):
     """More rows than workgroups at once, each with several runs a thread."""
