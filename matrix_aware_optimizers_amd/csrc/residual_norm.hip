@@ -230,10 +230,9 @@ template <typename TX, typename TB, int TPR, int V, int BLK, bool LDS>
 __global__ __launch_bounds__(BLK) void join_bwd_kernel(JoinBackArgs a) {
   constexpr int RPB = BLK / TPR, COLS = 4 * TPR * V;
   __shared__ float2 red[2][2][BLK / 64];
-  // parameters (the last one: the gate of each channel, or with gates of their own beta1); at
-  // the end the joining of the column sums
+  // parameters (the last one: the gate of each channel, or with gates of their own beta1)
   constexpr int AT = vectors_at(V, LDS);
-  __shared__ float vecs[AT == kInLds ? 3 : 1][AT == kInLds || RPB > 1 ? COLS : 1];
+  __shared__ float vecs[AT == kInLds ? 3 : 1][AT == kInLds ? COLS : 1];
   // a wavefront has one row
   int t = threadIdx.x % TPR;
   const int sub = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
@@ -471,35 +470,31 @@ __global__ __launch_bounds__(BLK) void join_bwd_kernel(JoinBackArgs a) {
   if (a.part == nullptr) return;
   // partial row of the workgroup: its row groups' sums in order 0, 1, ...
   float* out = a.part + (int64_t)blockIdx.x * 4 * a.cols;
-  float* join = vecs[0];
 #pragma unroll
   for (int which = 0; which < 4; ++which) {
     if constexpr (RPB > 1) {
-      for (int k = 0; k < RPB - 1; ++k) {
-        __syncthreads();
-        if (sub == k) {
+      __shared__ float join[RPB][COLS];
+      if (which > 0) __syncthreads();
 #pragma unroll
-          for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float* p = &join[(v * 4 + i) * TPR + t];
-              *p = k == 0 ? sums[which < S ? which : 0][v][i] : *p + sums[which < S ? which : 0][v][i];
-            }
-        }
+      for (int v = 0; v < V; ++v) {
+        const float(&w)[4] = sums[which < S ? which : 0][v];
+        *(float4*)&join[sub][4 * (t + v * TPR)] = make_float4(w[0], w[1], w[2], w[3]);
       }
       __syncthreads();
-    }
-    if (sub == RPB - 1) {
+      for (int c = threadIdx.x; c < a.cols; c += BLK) {
+        float w = join[0][c];
+#pragma unroll
+        for (int k = 1; k < RPB; ++k) w += join[k][c];
+        out[(int64_t)which * a.cols + c] = w;
+      }
+    } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = t + v * TPR;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float w = RPB > 1 ? join[RPB > 1 ? (v * 4 + i) * TPR + t : 0] : 0.f;
-          if (HALF && which >= 2)
-            w += rest[HALF ? which - 2 : 0][HALF ? 4 * c + i : 0];
-          else
-            w += sums[which < S ? which : 0][v][i];
+          const float w = HALF && which >= 2 ? rest[HALF ? which - 2 : 0][HALF ? 4 * c + i : 0]
+                                             : sums[which < S ? which : 0][v][i];
           if (4 * c + i < a.cols) out[(int64_t)which * a.cols + 4 * c + i] = w;
         }
       }
