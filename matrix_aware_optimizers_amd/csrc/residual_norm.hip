@@ -25,8 +25,8 @@
 //
 // Measured (bf16, both norms; a copy of 1 GiB reaches 5.2 TB/s): forward 16384 x 1536 40 us on
 // resident inputs (5.0 TB/s), 8192 x 4096 57 (4.7), 2048 x 16384 69 (3.9), one row of 1536 7, of
-// which the kernel is 3. Backward 16384 x 1536 70 us (4.3 TB/s, 4 of them the second kernel),
-// 8192 x 4096 88 (4.6), 4093 x 4096 with an fp32 stream and gates 77 (4.8), 4096 x 8192 with gates
+// which the kernel is 3. Backward 16384 x 1536 67 us (4.5 TB/s, 4 of them the second kernel),
+// 8192 x 4096 86 (4.7), 4093 x 4096 with an fp32 stream and gates 76 (4.9), 4096 x 8192 with gates
 // 116 (4.6), 2048 x 16384 181 (2.2: about 128 registers a thread are full, parameters come from the
 // L2 for each row; loads of a row held from its first pass to its second, 169, spilt more).
 #include "rows.hpp"
