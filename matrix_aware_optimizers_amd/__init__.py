@@ -4,10 +4,10 @@ and the layer operators that make their gradients (layer norm, linear layer,
 tokens and the loss).
 
 Thin binding over ``libmao.so`` (declared in ``include/mao.h``): ctypes for the
-steps, the C++ extension ``_layers.so`` for the layer operators and lists of tensors. The binding only
-marshals arguments: every step runs in the library's HIP
+steps, the C++ extension ``_layers.so`` for the layer operators and lists of tensors.
+The binding only marshals arguments: every step runs in the library's HIP
 kernels, on the current torch stream. PyTorch provides device memory and
-streams; the library itself allocates nothing, so the workspace is a torch
+streams; the library itself allocates none, so the workspace is a torch
 byte tensor allocated here and cached per device.
 
 If the library is missing, every call raises -- there is no CPU fallback.
