@@ -564,7 +564,7 @@ __global__ __launch_bounds__(THREADS) void token_loss_kernel(TokenBackArgs a) {
   const int pieces = (a.vocab + W - 1) / W, tid = threadIdx.x, row = blockIdx.x;
   const int64_t target = a.targets[row];
   const bool live = target >= 0;  // else nothing of the row matters
-  const int hit = target < a.vocab ? (int)target : -1;
+  const int hit = live && target < a.vocab ? (int)target : -1;
   // a row that does not matter is not read
   const auto x = row_buffer(a.x, a.ldx * (int64_t)sizeof(T), row, live ? pieces * 16 : 0);
   const RowOut<W> out(a.dx, a.dx_dtype, a.lddx, row, a.vocab);

@@ -453,3 +453,23 @@ def test_refusals(gpu_lib):
             call()
     only = lib.token_logprobs(X, entropy=False)
     assert only.logprob is None and only.entropy is None and torch.equal(only.stats, f.stats)
+
+
+@pytest.mark.parametrize("vocab", [5, 3000, 200003])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_targets_far_below_zero(gpu_lib, vocab, dtype):
+    """A target below 0 is none whatever its lower 32 bits say: nothing of its row counts."""
+    import torch
+    log(f"targets far below zero {vocab} {dtype}")
+    x, _ = _logits(4, 6, vocab)
+    X = _dev(x, dtype)
+    X[2] = float("nan")
+    t = _targets([-(1 << 32) + 3, -(1 << 63) + 1, -(1 << 40), -(1 << 63), -(1 << 32) + 4, 2])
+    f = gpu_lib.token_logprobs(X, t)
+    assert (f.logprob[:5] == 0).all() and f.logprob[5] != 0
+    one = torch.ones(6, device="cuda")
+    for w in (None, one):
+        lp, dx = gpu_lib.token_loss(X, t, w)
+        assert (lp[:5] == 0).all() and (dx[:5] == 0).all() and lp[5] != 0 and dx[5].any()
+    db = gpu_lib.token_logprobs_backward(X, t, f.stats, dlogprob=one)
+    assert (db[:5] == 0).all() and db[5].any()
