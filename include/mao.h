@@ -672,7 +672,7 @@ MAO_API mao_status mao_token_logprobs_backward(mao_mat X, const int64_t* targets
  * mao_token_loss -- logprob (NULL or rows floats) and the gradient of the loss
  * sum over rows of -weight logprob, in one pass: dX_j = weight (p_j - d_jt). weight: NULL (1)
  * or rows floats. dX: bf16 or fp32, may be X itself. A row without a target is not read; one of
- * weight 0 gets a gradient of zeros whatever it holds.
+ * weight 0 gets a gradient of zeros whatever it holds and whatever its target is.
  */
 MAO_API mao_status mao_token_loss(mao_mat X, const int64_t* targets, const float* weight,
                                   float* logprob, mao_mat dX, void* stream);

@@ -588,7 +588,7 @@ __global__ __launch_bounds__(THREADS) void token_loss_kernel(TokenBackArgs a) {
   // dx may be x: a thread writes what it alone has read
   q = block_sums<THREADS>(q, buf);
   float w = a.weight && live ? a.weight[row] : 1.f;
-  if (target >= a.vocab) w = NAN;
+  if (target >= a.vocab && w != 0.f) w = NAN;
   if (q.s == 0.f) w = 0.f;  // no finite logit
   const float scale = w / q.s;
   const bool nothing = !live || w == 0.f;

@@ -473,3 +473,17 @@ def test_targets_far_below_zero(gpu_lib, vocab, dtype):
         assert (lp[:5] == 0).all() and (dx[:5] == 0).all() and lp[5] != 0 and dx[5].any()
     db = gpu_lib.token_logprobs_backward(X, t, f.stats, dlogprob=one)
     assert (db[:5] == 0).all() and db[5].any()
+
+
+@pytest.mark.parametrize("vocab", [5, 3000, 200003])
+def test_weight_zero_outside_the_vocabulary(gpu_lib, vocab):
+    """A row of weight 0 gets zeros also where its target is outside the vocabulary."""
+    import torch
+    log(f"weight zero, target outside {vocab}")
+    x, _ = _logits(4, 4, vocab)
+    X = _dev(x, "bf16")
+    t = _targets([vocab, 1, vocab + 7, vocab])
+    lp, dx = gpu_lib.token_loss(X, t, torch.tensor([0.0, 1.0, -0.0, 1.0], device="cuda"))
+    assert torch.isnan(lp[[0, 2, 3]]).all() and torch.isfinite(lp[1])
+    assert (dx[[0, 2]] == 0).all() and torch.isnan(dx[3]).all()
+    assert torch.isfinite(dx[1]).all() and dx[1].any()
