@@ -661,7 +661,8 @@ MAO_API mao_status mao_token_logprobs(mao_mat X, const int64_t* targets, float* 
  * (each NULL or rows floats, one at least):
  *   dX_j = dlogprob (d_jt - p_j) + dlse p_j - dentropy p_j (log p_j + entropy)
  * stats (and entropy, with dentropy) as mao_token_logprobs gave them. dX: bf16 or fp32, may be
- * X itself. A row whose gradients are all 0 gets zeros whatever it holds.
+ * X itself. A row whose gradients are all 0 gets zeros whatever it holds. A target outside the
+ * vocabulary makes NaN of its row through a dlogprob other than 0 only.
  */
 MAO_API mao_status mao_token_logprobs_backward(mao_mat X, const int64_t* targets,
                                                const float* stats, const float* entropy,

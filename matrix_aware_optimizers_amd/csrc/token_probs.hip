@@ -504,7 +504,7 @@ __global__ __launch_bounds__(THREADS) void token_backward_kernel(TokenBackArgs a
   const int64_t target = a.targets ? a.targets[row] : -1;
   const float m = a.stats[2 * row], log_s = a.stats[2 * row + 1];
   float dlp = a.dlogprob && target >= 0 ? a.dlogprob[row] : 0.f;
-  if (target >= a.vocab) dlp = NAN;
+  if (target >= a.vocab && dlp != 0.f) dlp = NAN;
   const float dl = (a.dlse ? a.dlse[row] : 0.f) - dlp;
   const float de = ENT ? a.dentropy[row] : 0.f, h = ENT ? a.entropy[row] : 0.f;
   const bool empty = m == -INFINITY;

@@ -487,3 +487,25 @@ def test_weight_zero_outside_the_vocabulary(gpu_lib, vocab):
     assert torch.isnan(lp[[0, 2, 3]]).all() and torch.isfinite(lp[1])
     assert (dx[[0, 2]] == 0).all() and torch.isnan(dx[3]).all()
     assert torch.isfinite(dx[1]).all() and dx[1].any()
+
+
+@pytest.mark.parametrize("vocab", [5, 3000, 70000])
+def test_backward_outside_the_vocabulary(gpu_lib, vocab):
+    """A target outside the vocabulary makes NaN of its row through a gradient of its log
+    probability alone: one that is 0 or not given, and the others' gradients, do not know it."""
+    import torch
+    log(f"backward, target outside {vocab}")
+    x, _ = _logits(4, 3, vocab)
+    X = _dev(x, "bf16")
+    t, ok = _targets([vocab, 1, 2]), _targets([0, 1, 2])
+    f = gpu_lib.token_logprobs(X, ok)
+    one = torch.ones(3, device="cuda")
+    bw = gpu_lib.token_logprobs_backward
+    for kw in (dict(dlse=one), dict(dentropy=one, entropy=f.entropy)):
+        assert torch.equal(bw(X, t, f.stats, **kw), bw(X, None, f.stats, **kw))
+        zero = torch.tensor([0.0, 1.0, 1.0], device="cuda")
+        assert torch.equal(bw(X, t, f.stats, dlogprob=zero, **kw), bw(X, ok, f.stats, dlogprob=zero, **kw))
+    g = bw(X, t, f.stats, dlogprob=zero)
+    assert (g[0] == 0).all() and torch.equal(g, bw(X, ok, f.stats, dlogprob=zero))
+    g = bw(X, t, f.stats, dlogprob=one)
+    assert torch.isnan(g[0]).all() and torch.isfinite(g[1:]).all()
