@@ -505,11 +505,11 @@ __global__ __launch_bounds__(THREADS) void token_backward_kernel(TokenBackArgs a
   const float m = a.stats[2 * row], log_s = a.stats[2 * row + 1];
   float dlp = a.dlogprob && target >= 0 ? a.dlogprob[row] : 0.f;
   if (target >= a.vocab && dlp != 0.f) dlp = NAN;
-  const float dl = (a.dlse ? a.dlse[row] : 0.f) - dlp;
+  const float dlse = a.dlse ? a.dlse[row] : 0.f, dl = dlse - dlp;
   const float de = ENT ? a.dentropy[row] : 0.f, h = ENT ? a.entropy[row] : 0.f;
   const bool empty = m == -INFINITY;
   if (empty) dlp = 0.f;
-  const bool nothing = empty || (dl == 0.f && de == 0.f);
+  const bool nothing = empty || (dlp == 0.f && dlse == 0.f && de == 0.f);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int piece = lo + r * THREADS;

@@ -509,3 +509,23 @@ def test_backward_outside_the_vocabulary(gpu_lib, vocab):
     assert (g[0] == 0).all() and torch.equal(g, bw(X, ok, f.stats, dlogprob=zero))
     g = bw(X, t, f.stats, dlogprob=one)
     assert torch.isnan(g[0]).all() and torch.isfinite(g[1:]).all()
+
+
+@pytest.mark.parametrize("vocab", [5, 3000, 70000])
+def test_equal_gradients_of_a_row_of_nan(gpu_lib, vocab):
+    """Equal gradients of a row's log probability and of its log of the sum cancel in the
+    probabilities' factor; a row with a NaN or +inf has NaN all the same, any other one the
+    target's gradient alone."""
+    import torch
+    log(f"equal gradients {vocab}")
+    x, _ = _logits(4, 4, vocab)
+    X = _dev(x, "bf16")
+    X[1, 2], X[3, 0] = float("nan"), float("inf")
+    t = _targets([1, 2, 3, 4])
+    f = gpu_lib.token_logprobs(X, t)
+    two = torch.full((4,), 2.0, device="cuda")
+    g = gpu_lib.token_logprobs_backward(X, t, f.stats, dlogprob=two, dlse=two)
+    assert torch.isnan(g[[1, 3]]).all()
+    want = torch.zeros_like(g)
+    want[0, 1] = want[2, 3] = 2.0
+    assert torch.equal(g[[0, 2]], want[[0, 2]])
