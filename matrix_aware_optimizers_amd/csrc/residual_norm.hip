@@ -270,8 +270,8 @@ __global__ __launch_bounds__(BLK) void join_bwd_kernel(JoinBackArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) sums[k][v][i] = 0.f;
   const bool pre = a.pre.kind != MAO_ROW_NORM_NONE, post = a.post.kind != MAO_ROW_NORM_NONE;
-  const float pre_mean = a.pre.kind == MAO_ROW_NORM_LAYER ? inv_n : 0.f;
-  const float post_mean = a.post.kind == MAO_ROW_NORM_LAYER ? inv_n : 0.f;
+  const bool pre_mean = a.pre.kind == MAO_ROW_NORM_LAYER;
+  const bool post_mean = a.post.kind == MAO_ROW_NORM_LAYER;
   // One row in its stored form; a run of the next row is on its way as soon as this row's has
   // been used for the last time. (KEEP; else no registers are left for it, and each run is
   // loaded, from the cache after the first time, where it is used.)
@@ -370,7 +370,7 @@ __global__ __launch_bounds__(BLK) void join_bwd_kernel(JoinBackArgs a) {
       }
     }
     if (pre) group_total2<TPR>(s0, s1, buf[0]);
-    s0 *= pre_mean;
+    s0 = pre_mean ? s0 * inv_n : 0.f;  // chosen, not times 0: the sum may be infinite
     s1 *= inv_n;
     float p0 = 0.f, p1 = 0.f;
 #pragma unroll
@@ -432,8 +432,8 @@ __global__ __launch_bounds__(BLK) void join_bwd_kernel(JoinBackArgs a) {
     fetch(next);
     // without a norm of the block's output its gradient is p itself (mean 0, rstd 1)
     if (post) group_total2<TPR>(p0, p1, buf[1]);
-    p0 *= post_mean;
-    p1 *= post ? inv_n : 0.f;
+    p0 = post_mean ? p0 * inv_n : 0.f;
+    p1 *= inv_n;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int i0 = KEEP ? v : 0;

@@ -433,3 +433,28 @@ def test_refusals(gpu_lib):
             (lambda: lib.residual_norm_backward(h, x, b, r, st, out=r), E)):
         with pytest.raises(error):
             call()
+
+
+@pytest.mark.parametrize("cols", [30, 301, 1540, 5000, 9000])
+@pytest.mark.parametrize("types", [("bf16", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("gate", ["none", "vector", "matrix"])
+def test_not_finite_without_a_norm_of_the_block(gpu_lib, cols, types, gate):
+    """Without a norm of the block's output its gradient is made element by element: a NaN or an
+    infinity in one leaves all the others alone."""
+    import torch
+    log(f"not finite, no post norm {cols} {types} {gate}")
+    for pre in ("none", "rms"):
+        c = Case(cols, 5, cols, *types, "none", pre, gate)
+        r, _, st = gpu_lib.residual_norm(c.X, c.B, **c.kw)
+        call = lambda: gpu_lib.residual_norm_backward(  # noqa: E731
+            None if pre == "none" else c.dH, c.dR, c.B, None if pre == "none" else r, st, sums=False,
+            **c.back_kw())
+        want = call()
+        at = torch.zeros((5, cols), dtype=torch.bool, device="cuda")
+        for k, bad in enumerate((float("inf"), -float("inf"), float("nan"))):
+            c.dR[k, 7 * k + 8] = bad
+            at[k, 7 * k + 8] = True
+        got = call()
+        for p, q in ((got.dX, want.dX), (got.dB, want.dB)) + (((got.dgate, want.dgate),) if gate == "matrix" else ()):
+            assert torch.equal(p[~at], q[~at])
+            assert not torch.isfinite(p[at].float()).any()
