@@ -551,8 +551,9 @@ __global__ __launch_bounds__(1024) void join_sums_kernel(JoinBackArgs a, int blo
   if (a.dpost_beta) a.dpost_beta[col] = a.bs * g * s.y;
   if (a.dgate_vec) {
     const float gam = a.post.gamma ? load1_any(a.post.gamma, a.post.p_dtype, col) : 1.f;
-    const float bet = a.post.beta ? load1_any(a.post.beta, a.post.p_dtype, col) : 0.f;
-    a.dgate_vec[col] = a.bs * (gam * s.x + bet * s.y);
+    float w = gam * s.x;
+    if (a.post.beta) w += load1_any(a.post.beta, a.post.p_dtype, col) * s.y;  // s.y may be infinite
+    a.dgate_vec[col] = a.bs * w;
   }
 }
 

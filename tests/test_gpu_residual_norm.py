@@ -458,3 +458,21 @@ def test_not_finite_without_a_norm_of_the_block(gpu_lib, cols, types, gate):
         for p, q in ((got.dX, want.dX), (got.dB, want.dB)) + (((got.dgate, want.dgate),) if gate == "matrix" else ()):
             assert torch.equal(p[~at], q[~at])
             assert not torch.isfinite(p[at].float()).any()
+
+
+@pytest.mark.parametrize("post", ["none", "rms", "layer"])
+def test_infinite_gradient_of_a_gate_vector(gpu_lib, post):
+    """One infinite dR makes its column's gate gradient infinite, of the sign that the formula gives;
+    the other columns keep theirs."""
+    import torch
+    log(f"infinite gate gradient {post}")
+    c = Case(5, 40, 301, "f32", "f32", post, "none", "vector")
+    c.kw.pop("post_beta", None)  # no offset: the gradient is the sum of dR xh gamma alone
+    r, _, st = gpu_lib.residual_norm(c.X, c.B, **c.kw)
+    want = gpu_lib.residual_norm_backward(None, c.dR, c.B, None, st, **c.back_kw()).dgate
+    c.dR[7, 33] = float("inf")
+    got = gpu_lib.residual_norm_backward(None, c.dR, c.B, None, st, **c.back_kw()).dgate
+    xh = (c.B[7, 33] - st[7, 0]) * st[7, 1] * (c.kw["post_gamma"][33] if post != "none" else 1.0)
+    assert got[33] == c.bs * xh * float("inf")
+    keep = torch.arange(301, device="cuda") != 33
+    assert torch.equal(got[keep], want[keep])
