@@ -529,3 +529,36 @@ def test_equal_gradients_of_a_row_of_nan(gpu_lib, vocab):
     want = torch.zeros_like(g)
     want[0, 1] = want[2, 3] = 2.0
     assert torch.equal(g[[0, 2]], want[[0, 2]])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_loss_of_rows_read_twice(gpu_lib, dtype):
+    """Rows beyond the registers, of both types: values against float64."""
+    log(f"loss of long rows {dtype}")
+    rows, vocab = 4, 200003
+    x, t = _logits(8, rows, vocab, masked=vocab // 5)
+    t = np.where(np.isinf(x[np.arange(rows), np.maximum(t, 0)]), -1, t)
+    t[0] = int(np.argmax(x[0]))
+    X, T = _dev(x, dtype), _targets(t)
+    x = _host(X)
+    import torch
+    a = np.random.default_rng(9).standard_normal(rows).astype(np.float32).astype(np.float64)
+    lp, dx = gpu_lib.token_loss(X, T, torch.from_numpy(a.astype(np.float32)).cuda())
+    zero = np.zeros(rows)
+    _check_gradient(dx, x, t, -a, zero, zero, dtype)
+    want = ref.forward(x, t)
+    assert (np.abs(_host(lp) - want[0]) <= (170 + 2 * np.abs(want[0]) + 6 * np.abs(want[3])) * R).all()
+
+
+@pytest.mark.parametrize("vocab", [9000, 50304, 70000])
+@pytest.mark.parametrize("offset", [256.0, -4096.0, 1e6])
+def test_alternatives_of_rows_with_an_offset(gpu_lib, vocab, offset):
+    """fp32 logits far from 0, no two alike but by chance: thousands share the upper 16 bits."""
+    log(f"alternatives, offset {offset} {vocab}")
+    x, t = _logits(vocab, 5, vocab)
+    X = _dev(x + offset, "f32")
+    got = gpu_lib.token_logprobs(X, _targets(t), top=20)
+    assert np.array_equal(got.top_ids.cpu().numpy(), ref.top(_host(X), 20))
+    want = np.take_along_axis(ref.forward(_host(X), t)[4], ref.top(_host(X), 20), axis=1)
+    # y = x - M is exact here or off by r |y|, as always: the offset does not count
+    assert (np.abs(_host(got.top_logprobs) - want) <= (400 + 4 * np.abs(want)) * R).all()
