@@ -435,6 +435,9 @@ typedef struct {
  * 8-bit states are rounded up or down by a fixed dither of element index and t, unbiased over
  * the steps, so that averages move by less than a code's step too. 256 elements whose m or v
  * holds a NaN or an infinity read as NaN from then on.
+ * t and all other host arguments are the call's own: a captured call repeats them at every
+ * replay, its bias corrections and its dither too. 8-bit averages then can stand still, several
+ * codes from their value: such a step is called outside the graph, or captured again for each t.
  */
 MAO_API mao_status adamw_step_many(int32_t count, const mao_adamw_tensor* tensors, int64_t t,
                                    float beta1, float beta2, float eps, const float* grad_scale,

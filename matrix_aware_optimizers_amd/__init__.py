@@ -760,7 +760,9 @@ def adamw_step_many(items, t: int, *, lr, beta1=0.9, beta2=0.95, eps=1e-8, weigh
     """adamw_step on many tensors in one call. ``items``: tuples (w, g, m, v) with fp32 states
     or (w, g, m, m_scale, v, v_scale) with 8-bit ones (``adamw8_state``), contiguous tensors
     of one device. ``lr`` and ``weight_decay``: a number, or a list with one per tensor.
-    ``grad_scale``: a device fp32 scalar that every gradient is multiplied by."""
+    ``grad_scale``: a device fp32 scalar that every gradient is multiplied by. A captured call
+    repeats its ``t`` at every replay, with its bias corrections and the 8-bit states' dither, under
+    which averages can stand still: call it outside the graph, or capture it for each ``t``."""
     if len(items) == 0:
         raise ValueError("adamw_step_many needs at least one tensor")
     _run("adamw_step_many", items[0][0], items, t, lr, beta1, beta2, eps, weight_decay, grad_scale)

@@ -166,3 +166,41 @@ def test_oracle_round_trip_and_average(which):
         total += v
     # an element's dithers are the sequence shifted by its index: the same discrepancy times 2
     assert (np.abs(total / steps - x) <= 2 * disc * step).all()
+
+
+def _fast_dither(n, which, t):
+    """adam8.dither without Python's whole numbers: sums modulo 2^64, of which 2^32 divides."""
+    a, b = adam8.DITHER[which]
+    cut = 32 - 23 + adam8.MANTISSA[which]
+    d = (np.arange(n, dtype=np.uint64) * np.uint64(a) + np.uint64(t * b % (1 << 32))) & np.uint64(0xFFFFFFFF)
+    return (d >> np.uint64(cut)).astype(np.float64) * 0.5 ** (32 - cut)
+
+
+def _store(x, which, t):
+    """What a state that is to hold x holds, and its scales."""
+    codes, scales = adam8.encode(x, which, t)
+    return adam8.decode(codes, scales, which), scales
+
+
+def test_oracle_dither_of_a_step_that_stands_still(monkeypatch):
+    """A replayed graph repeats its t, and with it every element's dither d. A code then goes down
+    only where (1 - beta1) of what is too much, in steps of the code, is above d: for 30% too much
+    that is 0.1 0.3 / 1.3 of m, of which a step is 1/8 to 1/16, so 0.18 to 0.37. The dithers being
+    equally spread, more than half of the elements stay where they are. As t advances all come
+    down, to within a step of their value on average. What mao.h says of captured steps."""
+    assert all((_fast_dither(777, k, 91) == adam8.dither(777, k, 91)).all() for k in "mv")
+    monkeypatch.setattr(adam8, "dither", _fast_dither)
+    g = np.exp(np.random.default_rng(1).uniform(np.log(0.05), np.log(0.7), 2048))
+    g[::256] = 1.0  # holds its span's scale
+    start = np.where(g == 1.0, 1.0, 1.3 * g)
+
+    def last_steps(frozen):
+        m, mean = start, np.zeros(g.size)
+        for t in range(1, 301):
+            m = _store(0.9 * m + 0.1 * g, "m", frozen or t)[0]
+            mean += m / 150 if t > 150 else 0.0
+        return mean
+
+    assert (np.abs(last_steps(None) / g - 1) <= 1 / 8).all()
+    for frozen in (4, 100):
+        assert (last_steps(frozen) > 1.15 * g).mean() > 0.5
