@@ -7,7 +7,8 @@
 // and a mantissa of 3 bits (m, with a sign) or 4 bits (r, never negative), times one fp32
 // scale per 256 elements that makes the largest of them the largest code. sqrt(v), not v:
 // the denominator's relative error is what matters, and half the exponent range covers it. A
-// nonzero r has a code of at least 1, so that no update is divided by eps alone.
+// nonzero r has a code of at least 1, so that no update is divided by eps alone; an r below that
+// code, 2^-19 of its span's largest, gives smaller updates than its own.
 //
 // Rounding: an average of many steps moves by less than half a code's step at a time, and
 // rounding to the nearest would hold it where it is. What is cut off is rounded up with
@@ -16,7 +17,9 @@
 // the top of (a i + b t) mod 2^32, an additive recurrence (Kronecker's sequence; a and b
 // are 2^32 times the golden ratio's fraction and times that of the next such ratio), equally
 // spread over the steps of one element and over the elements of one step. No random
-// state, the same results for the same inputs.
+// state, the same results for the same inputs. It leaves r, not r^2, where it is on average: r^2
+// gains each rounding's variance, up to 3% in all at beta2 = 0.999 (a rounding's variance is at
+// most a code's step, r / 16, times what r moves in a step).
 //
 // A span of 256 whose m or r holds a NaN or an infinity gets a NaN scale: all of it reads as
 // NaN. A span whose largest m is below 2^-100 counts as zeros.

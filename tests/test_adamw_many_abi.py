@@ -204,3 +204,34 @@ def test_oracle_dither_of_a_step_that_stands_still(monkeypatch):
     assert (np.abs(last_steps(None) / g - 1) <= 1 / 8).all()
     for frozen in (4, 100):
         assert (last_steps(frozen) > 1.15 * g).mean() > 0.5
+
+
+@pytest.mark.parametrize("spread", [0.5, 1.0, 3.0])
+def test_oracle_second_moment_of_random_gradients(monkeypatch, spread):
+    """beta2 = 0.999, gradients of magnitudes that differ within a span. The dither leaves r as it is
+    on average, so r^2 gains the variance f (1 - f) step^2 of each rounding, where f step is at most
+    what r moves in a step: (1 - beta2) / 2 |g^2 / v - 1| r, on average 0.97 times the first
+    factor (normal g). A step is at most r / 16, so v gains 3e-5 of itself a step and 0.0303 over the
+    1000 that it remembers. Elements whose r is below the smallest code, 2^-18 of the scale, hold
+    that code instead."""
+    monkeypatch.setattr(adam8, "dither", _fast_dither)
+    n, steps, warm, b2 = 1024, 5000, 2500, 0.999
+    rng = np.random.default_rng(3)
+    s = np.exp(spread * rng.standard_normal(n))
+    v, r, want, got = (np.zeros(n) for _ in range(4))
+    for t in range(1, steps + 1):
+        g = s * rng.standard_normal(n)
+        v = b2 * v + (1 - b2) * g * g
+        r, scales = _store(np.sqrt(b2 * r * r + (1 - b2) * g * g), "v", t)
+        if t > warm:
+            want += v
+            got += r * r
+    ratio, scale = got / want, np.repeat(scales, 256)
+    whole = np.sqrt(v) >= 2.0 ** -13 * scale  # codes that have all their bits, and stay there
+    assert whole.mean() > 0.5
+    # four standard deviations of the mean
+    assert abs(ratio[whole].mean() - 1 - 0.0303 / 2) < 0.0303 / 2 + 4 * ratio[whole].std() / whole.sum() ** 0.5
+    assert (r >= 2.0 ** -18 * scale * (1 - 1e-12)).all()
+    if spread == 3.0:
+        low = np.sqrt(v) < 2.0 ** -20 * scale
+        assert low.any() and (ratio[low] > 2).all()
