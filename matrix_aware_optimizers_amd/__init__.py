@@ -757,7 +757,7 @@ def adamw8_state(w):
 
 def adamw_step_many(items, t: int, *, lr, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.0,
                     grad_scale=None):
-    """adamw_step on many tensors in one call. ``items``: tuples (w, g, m, v) with fp32 states
+    """adamw_step on up to 4096 tensors in one call. ``items``: tuples (w, g, m, v) with fp32 states
     or (w, g, m, m_scale, v, v_scale) with 8-bit ones (``adamw8_state``), contiguous tensors
     of one device. ``lr`` and ``weight_decay``: a number, or a list with one per tensor.
     ``grad_scale``: a device fp32 scalar that every gradient is multiplied by. A captured call
