@@ -128,7 +128,8 @@ template <int CTRL> __device__ __forceinline__ uint32_t dpp_max(uint32_t x) {
 }
 
 // Codes of 8 values (elements first, first + 1, ...) and the scale of the span that the 32
-// lanes around this one hold.
+// lanes around this one hold. Quotients are rounded to nearest, not the hardware's reciprocal: a
+// last bit decides a code where a border is near.
 template <bool SIGNED>
 __device__ __forceinline__ uint2 adam8_encode(const float (&v)[8], uint32_t first, uint32_t step,
                                               float& scale) {
@@ -146,14 +147,22 @@ __device__ __forceinline__ uint2 adam8_encode(const float (&v)[8], uint32_t firs
   const bool bad = top >= 0x7f800000u;
   const bool live = largest >= 0x1p-100f && !bad;
   scale = bad ? __uint_as_float(0x7fc00000u) : live ? largest * (1.f / F::kMax) : 0.f;
-  const float inv = live ? F::kMax * __builtin_amdgcn_rcpf(largest) : 0.f;
+  float inv = 0.f;
+  if (live) {
+    inv = __builtin_amdgcn_rcpf(largest);
+    inv = __builtin_fmaf(__builtin_fmaf(-largest, inv, 1.f), inv, inv) * F::kMax;
+    if (largest > 0x1p120f) inv = 1.f / largest * F::kMax;  // a reciprocal near the end of the range
+  }
   uint32_t c[2] = {0, 0};
   const uint32_t d0 = first * F::kElement + step * F::kStep;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float y = fabsf(v[i]) * inv * 0x1p-112f;
+    // y's places from the code's on down: its own bits, or among the subnormals (below 2^-14)
+    // whole multiples of 2^-37
+    const float y = fabsf(v[i]) * inv;
+    const uint32_t places = y < 0x1p-14f ? (uint32_t)(y * 0x1p37f) : __float_as_uint(y) - (112u << 23);
     const uint32_t d = (d0 + (uint32_t)i * F::kElement) >> (32 - F::kDrop);
-    uint32_t k = min((__float_as_uint(y) + d) >> F::kDrop, F::kTop);
+    uint32_t k = min((places + d) >> F::kDrop, F::kTop);
     if (SIGNED)
       k |= __float_as_uint(v[i]) >> 24 & 128u;
     else

@@ -413,3 +413,65 @@ def test_far_offsets(gpu_lib):
     assert ((m1 - gf).abs() <= torch.maximum(gf.abs() / 8, st[1][-3:].repeat_interleave(256)[:tail] * 2.0 ** -17) * 1.001).all()
     del w, g, st
     torch.cuda.empty_cache()
+
+
+def _encode32(x, which, t):
+    """Codes and scales of fp32 x, each operation rounded by itself (numpy's float32)."""
+    f = np.float32
+    n, k = x.size, adam8.MANTISSA[which]
+    top = f(2.0 - 0.5 ** k)
+    pad = np.zeros((n + 255) // 256 * 256, f)
+    pad[:n] = np.abs(x)
+    largest = pad.reshape(-1, 256).max(axis=1)
+    live = largest >= f(2.0 ** -100)
+    with np.errstate(divide="ignore", over="ignore", invalid="ignore"):
+        inv = np.where(live, f(1) / largest * top, f(0))
+    scales = np.where(live, largest * (f(1) / top), f(0))
+    y = pad * np.repeat(inv, 256)
+    drop = 23 - k
+    a, b = adam8.DITHER[which]
+    i = np.arange(pad.size, dtype=np.uint64)
+    d = ((i * np.uint64(a) + np.uint64(t * b % (1 << 32))) & np.uint64(0xFFFFFFFF)) >> np.uint64(32 - drop)
+    # the code's places with `drop` bits below them, cut off: a float's own bits, or, among the
+    # subnormals, the multiple of 2^-37
+    whole = y.view(np.int32).astype(np.int64) - (112 << 23)
+    places = np.where(y < f(2.0 ** -14), np.floor(y.astype(np.float64) * 2.0 ** 37).astype(np.int64), whole)
+    code = ((places + d.astype(np.int64)) >> drop)[:n]
+    if which == "m":
+        return np.minimum(code, 127) | np.where(np.signbit(x), 128, 0), scales
+    return np.where((x > 0) & np.repeat(live, 256)[:n], np.clip(code, 1, 255), 0), scales
+
+
+@pytest.mark.parametrize("g,clip", [("f32", False), ("bf16", True)])
+def test_8bit_states_are_the_formulas(gpu_lib, g, clip):
+    """States equal, bit for bit, what the formula's operations give, each rounded to fp32 by
+    itself: a last bit more or less of m, r or a scale would be a whole code's step where a border
+    is near, once in 2^20 elements, and w another one from the next step on."""
+    import torch
+    log(f"8-bit states as the formula {g}")
+    f = np.float32
+    n = 3_000_001
+    mc, ms, vc, vs = _state8(5, n)
+    ms[:3], vs[3:5] = (1e-30, 3e37, 2e-29), (1e-15, 1e-13)
+    W, dev = _rand(1, n), [torch.from_numpy(a).cuda() for a in (mc, ms, vc, vs)]
+    factor = torch.tensor(0.37, device="cuda") if clip else None
+    m = adam8.decode(mc, np.ones(ms.size), "m").astype(f) * np.repeat(ms, 256)[:n]
+    r = adam8.decode(vc, np.ones(vs.size), "v").astype(f) * np.repeat(vs, 256)[:n]
+    b1, b2 = f(0.9), f(0.95)
+    for t in (12, 13):
+        G = _rand(t, n, g, 0.01)
+        G[::1000] = 0.0
+        x = G.float().cpu().numpy()
+        if clip:
+            x = x * f(0.37)
+        gpu_lib.adamw_step_many([(W, G, *dev)], t, grad_scale=factor, **HP)
+        m = b1 * m + (f(1) - b1) * x
+        r = np.sqrt(b2 * (r * r) + (f(1) - b2) * x * x)
+        assert m.dtype == r.dtype == f
+        for k, (z, which) in enumerate(((m, "m"), (r, "v"))):
+            codes, scales = _encode32(z, which, t)
+            assert np.array_equal(dev[2 * k + 1].cpu().numpy(), scales), which
+            got = dev[2 * k].cpu().numpy().astype(np.int64)
+            assert (got != codes).sum() == 0, which
+            value = adam8.decode(codes, np.ones(scales.size), which).astype(f)
+            z[:] = value * np.repeat(scales, 256)[:n]
