@@ -24,11 +24,18 @@
 // leave as one partial row; a second kernel adds those in order. No atomics, fp32.
 //
 // Measured (bf16, both norms; a copy of 1 GiB reaches 5.2 TB/s): forward 16384 x 1536 40 us on
-// resident inputs (5.0 TB/s), 8192 x 4096 57 (4.7), 2048 x 16384 69 (3.9), one row of 1536 7, of
-// which the kernel is 3. Backward 16384 x 1536 67 us (4.5 TB/s, 4 of them the second kernel),
-// 8192 x 4096 86 (4.7), 4093 x 4096 with an fp32 stream and gates 76 (4.9), 4096 x 8192 with gates
-// 116 (4.6), 2048 x 16384 181 (2.2: about 128 registers a thread are full, parameters come from the
-// L2 for each row; loads of a row held from its first pass to its second, 169, spilt more).
+// resident inputs (5.0 TB/s), 8192 x 4096 57 (4.7), 2048 x 16384 69 (3.9), one row of 1536 7 (host
+// time; the kernel is 4.2 to 4.4 under the profiler). Backward 16384 x 1536 68 us (4.5 TB/s, 4 of
+// them the second kernel), 8192 x 4096 86 (4.7), 4093 x 4096 with an fp32 stream and gates 76 (4.9),
+// 4096 x 8192 with gates 116 (4.6), 2048 x 16384 172 (2.3: 128 registers a thread are full,
+// parameters come from the L2 for each row; loads of a row held from its first pass to its
+// second spilt more). One row of 1536 13 (kernels 7.4 and 2.6, the rest host time).
+// Forms of 1024 threads that spill, of their 128 registers (stream, block): backward above 8192
+// columns 4 to 11 in all types, 6145 to 8192 10 (bf16, fp32) and 20 (both fp32); forward above 8192
+// 4 and 11 of the same two. Two rms norms, forward and backward, bf16 / fp32 stream / fp32 block /
+// both fp32: 4096 x 8192 59 and 93 us / 81 and 126 / 81 and 128 / 98 and 171 (4.6 to 5.5 TB/s, 4.3 to
+// 4.8); 2048 x 12288 59 and 133 / 73 and 158 / 79 and 172 / 108 and 198 (3.4 to 4.1, 2.3 to 3.1);
+// 2048 x 16384 65 and 171 / 90 and 194 / 99 and 209 / 127 and 240 (4.0 to 4.5, 2.3 to 3.4).
 #include "rows.hpp"
 
 #include <algorithm>
@@ -37,7 +44,14 @@ namespace mao {
 
 namespace {
 
-// Results that would push everything else out of the L2s (32 MB) go past them.
+// Large results go past the caches. Measured on both sides, us, through them / past them, two rms
+// norms forward (with a reading of h right after): bf16 2048 x 1536 8.3 / 6.9 (12.6 / 11.5), 5461 x
+// 1536, the limit, 17.4 / 15.6 (23.6 / 23.7), 16384 x 1536 41.3 / 35.7 (56.6 / 59.9), 8192 x 4096
+// 63.4 / 55.3 (85.4 / 90.6); fp32 5461 x 1536 20.9 / 20.9 (31.2 / 34.0), 16384 x 1536 76.1 / 73.4
+// (109.7 / 117.3). Backward 16384 x 1536 bf16 67.4 / 60.4 (with a reading of dB 84.5 / 86.2), 2048 x
+// 4096, the limit, 28.9 / 29.4 (34.8 / 36.9). So the call gains up to 14%, and a next reader pays that
+// back and up to 9% of the two on top. The limit is the size at which two bf16 results fill the
+// L2s (32 MB); no size divides gain from loss.
 __device__ __forceinline__ bool past_l2(int rows, int cols) {
   return (int64_t)rows * cols >= (int64_t)1 << 23;
 }

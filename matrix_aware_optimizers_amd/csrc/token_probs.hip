@@ -18,7 +18,8 @@
 // and the latency of one row, the rest by HBM (a copy of 1 GiB reaches 5.2 TB/s).
 //
 // Measured: forward bf16 16384 x 50304 269 us (6.1 TB/s), 4096 x 50304 with 20 alternatives 91
-// (4.5), one row of 50304 6.6, with 20 alternatives 9.3; 77 rows 9.6. Backward bf16 8192 x 50304
+// (4.5), one row of 50304 6.6, with 20 alternatives 9.3; 77 rows 9.6; fp32 4096 x 50304 136 (6.1),
+// with 20 alternatives 147 (5.6), one row 6.0 and 9.0. Backward bf16 8192 x 50304
 // 270 us (6.1 TB/s), fp32 2045 x 50301 141 (5.8). Loss bf16 16384 x 50304 533 us (6.2 TB/s),
 // 4096 x 128256 392 (5.4), 2048 x 256000 485 (4.3, or 6.5 with the second reading that bf16 rows
 // beyond 196608 columns, fp32 ones beyond 98304, take), fp32 4096 x 50304 288 (5.7).
@@ -441,8 +442,13 @@ template <typename T> struct Piece {
   }
 };
 
-// A row of results, written past the L2 (the next reader is another kernel, and the rows are
-// larger): 16384 x 50304 bf16 555 us for 577 when it was measured, 16384 x 8000 90 for 102.
+// A row of results, written past the caches at every size: us, past them / through them, bf16, (with
+// a reading of the gradient right after): loss 16 x 50304 8.9 / 8.9 (11.2 / 11.1), 256 x 50304 10.8 /
+// 12.8 (21.5 / 21.1), 1024 x 50304 32.3 / 44.1 (78.5 / 77.2), 4096 x 50304 141 / 147 (310 / 301),
+// 16384 x 8000 90 / 95 (203 / 194); gradient of log probabilities 16 x 50304 3.5 / 3.8 (7.1 / 7.1),
+// 256 x 50304 6.8 / 10.3 (20.5 / 19.0), 16384 x 8000 75 / 93 (197 / 190). So the call gains up to a
+// third, and a reader that follows at once pays it back and up to 10% of the two on top (1024 x
+// 50304, gradient: 72.1 / 79.4): no size divides gain from loss.
 template <int W> struct RowOut {
   char* p;
   int dtype, cols;
@@ -645,9 +651,15 @@ mao_status forward_go(const TokenArgs& a, hipStream_t s) {
 //   50304: 256 threads 7.4 / 11.8 (1 row), 20.6 / 28.0 (1024 rows); 512 threads 6.4 / 9.4, 20.1 /
 //   26.0; 1024 threads 6.6 / 10.2, 24.1 / 39.2
 //   20000: 256 threads 11.2 / 15.6 (1024 rows), 512 threads 13.2 / 18.8
-// A row over four workgroups and a second kernel to join them took 10 / 11.7 on one row of
-// 50304, gained nothing below 128256 columns or above 256 rows, and was left out (one row of
-// 256000, where a CU's arithmetic bounds it: 10 / 16 for 19 / 23).
+// Above 65536, 512 threads and 1024, at 128 rows, 256 and 320 (a second row on some CUs):
+//   65544: 8.0 / 11.2 and 7.5 / 11.1, 9.1 / 12.1 and 8.9 / 12.5, 13.0 / 16.7 and 13.1 / 20.3
+//   128256: 12.9 / 17.0 and 11.8 / 15.6, 13.9 / 18.6 and 13.4 / 17.2, 21.4 / 27.2 and 21.5 / 28.8
+//   256000: 23.4 / 29.4 and 20.8 / 25.2, 24.2 / 32.6 and 23.2 / 27.6, 41.2 / 50.1 and 42.2 / 50.2
+//   (one row: 65544 7.1 / 10.0 and 6.8 / 10.4, 256000 20.3 / 24.7 and 18.8 / 22.7)
+// A row over four workgroups and a second kernel to join them took 10 / 11.7 on one row of 50304 and
+// gained nothing below 128256 columns or above 256 rows; one row of 256000, which a CU's
+// arithmetic bounds, took 10 / 16 for 19 / 23. Left out: chosen here, for those sizes alone, it would
+// cost the other calls nothing, and those two kernels more.
 template <typename T>
 mao_status forward_pick(const TokenArgs& a, hipStream_t s) {
   const int64_t runs = ceil_div(a.vocab, 8);
