@@ -436,9 +436,10 @@ typedef struct {
  * move by less than a code's step too. Over the steps it leaves m and r = sqrt(v) where they are
  * on average; v, read as r^2, is up to 3% high on average at beta2 = 0.999. A nonzero r is held
  * as 2^-18 of its scale (2^-19 of the largest of its 256) at least: elements with smaller ones get
- * smaller steps than theirs. m, r and their codes are made of single fp32 operations, each rounded
- * to nearest, in the order of the formulas. 256 elements whose m or v holds a NaN or an infinity
- * read as NaN from then on.
+ * smaller steps than theirs. m, r and their codes are made of single fp32 operations in the order
+ * of the formulas, each rounded to nearest (square roots and reciprocals of the largest but for
+ * about one in a million). 256 elements whose m or v holds a NaN or an infinity read as NaN from
+ * then on.
  * t and all other host arguments are the call's own: a captured call repeats them at every
  * replay, its bias corrections and its dither too. 8-bit averages then can stand still, several
  * codes from their value: such a step is called outside the graph, or captured again for each t.
